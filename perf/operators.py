@@ -357,8 +357,10 @@ def _plain_fork(st):
     L = torch.where(parent >= 0, lens[p], 0)
     n = (L + P - 1) // P
     row = torch.where(torch.arange(Np, device="cuda") < n[:, None], table[p], -1)
-    earlier = (parent[:, None] == parent) & (torch.arange(B, device="cuda") < torch.arange(B, device="cuda")[:, None])
-    copies = (parent >= 0) & (L % P != 0) & earlier.any(1)
+    # a partial last page stays with the parent's own row, else with the first row that continues it
+    me = torch.arange(B, device="cuda")
+    earlier = ((parent[:, None] == parent) & (me < me[:, None])).any(1)
+    copies = (parent >= 0) & (L % P != 0) & (parent != me) & (earlier | (parent[p] == p))
     last = (n - 1).clamp_min(0).long()[:, None]
     src = row.gather(1, last)[:, 0].long()
     dst = fresh[(copies.long().cumsum(0) - 1).clamp_min(0)]
