@@ -18,8 +18,9 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
-SOURCES = ["api.cu", "meta.cu", "score.cu", "select.cu", "decode.cu"]
-HEADERS = ["common.cuh", "internal.h", "pipeline.cuh", "record.cuh"]
+SOURCES = ["api.cu", "meta.cu", "score.cu", "select.cu", "decode.cu", "kv4_rows.cu", "kv4_decode.cu", "pages.cu"]
+PUBLIC = ["entmaxkv.h", "entmaxkv_kv4.h", "entmaxkv_pages.h"]
+HEADERS = ["common.cuh", "entmax.cuh", "internal.h", "pipeline.cuh", "record.cuh", "kv4.cuh"]
 
 
 def _newer(target, deps):
@@ -31,7 +32,7 @@ def _newer(target, deps):
 
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "entmaxkv.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", h) for h in PUBLIC]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -21,6 +21,10 @@ std::mutex g_mu;
 DevInfo g_dev[MAX_DEV];
 bool g_dev_ok[MAX_DEV];
 
+}  // namespace
+
+namespace ekv {
+
 int device_info(DevInfo *out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) return ENTMAXKV_ERR_CUDA;
@@ -37,6 +41,10 @@ int device_info(DevInfo *out) {
     *out = g_dev[dev];
     return ENTMAXKV_OK;
 }
+
+}  // namespace ekv
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
@@ -104,9 +112,9 @@ int make_kv_map_uncached(CUtensorMap *m, const void *base, const entmaxkv_shape 
     return r == CUDA_SUCCESS ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-constexpr int MAX_SEL_PAGES = 196608;
+namespace ekv {
 
 int check_shape(const entmaxkv_shape *s) {
     if (!s) return ENTMAXKV_ERR_NULL;
@@ -137,6 +145,10 @@ int integer_r(float alpha) {
     if (ri >= 1.0 && ri <= 8.0 && std::fabs(r - ri) <= 1e-5 * ri) return (int)ri;
     return 0;
 }
+
+}  // namespace ekv
+
+namespace {
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
 

@@ -34,6 +34,7 @@
 // pv_stream_kernel, which streams every V tile through the TMA ring.  Full-cache softmax runs softmax_kernel (K and V
 // tiles per stage, online max / sum per split); both dense paths combine
 // their splits in a fixed order in the last CTA of each group.
+#include "entmax.cuh"
 #include "pipeline.cuh"
 
 namespace ekv {
@@ -731,86 +732,6 @@ inline int tau_zcap(int ctas, int sms) {
     return z;
 }
 
-// The entmax threshold: the root t of sum_c [z_c - t]_+^r = 1 over the
-// candidates (every token with weight has z > z_max - 1), which lies in
-// [lo, hi] = [z_max - 1, z_max - n^(1-alpha)] where F(t) = sum - 1 decreases.
-// Newton's method, for r >= 1 (alpha <= 2) on g(t) = (sum_c [z_c - t]_+^r)^(1/r),
-// a norm of (z - t)_+ and so convex (one step when the support's z are equal),
-// from the left end; for r < 1 on F, which is then concave, from the right
-// end: either way the iterates move to the root monotonically.
-// for_each(add, first, stride) calls add(z) on candidates first, first +
-// stride, ...  With n candidates, n <= TAU_WARP_MAX, warp 0 runs every pass
-// by itself (lane-strided sums, a shuffle butterfly) and hands t to the other
-// warps with one barrier at the end.  Otherwise each thread takes a
-// TAU_NT-strided share and the warps' sums are added in warp order
-// (reproducible), one barrier per pass (red is double-buffered).  All TAU_NT
-// threads call it and return the same t.
-constexpr int TAU_WARP_MAX = 256;
-template <class ForEach>
-__device__ float entmax_tau(ForEach for_each, int n, float lo, float hi, float zmax, float r, int ri,
-                            float (*red)[TAU_NW][2]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool per_warp = n <= TAU_WARP_MAX;
-    const int first = per_warp ? lane : (int)threadIdx.x, stride = per_warp ? 32 : TAU_NT;
-    const float tol = 1e-7f * fmaxf(1.f, fabsf(zmax));
-    const int rim1 = ri >= 2 ? ri - 1 : 0;
-    float t = r >= 1.f ? lo : hi;
-    for (int it = 0; it < 40 && (!per_warp || warp == 0); ++it) {
-        float s0 = 0.f, s1 = 0.f;  // sum x^r, sum x^(r-1) over x = z - t > 0
-        auto add = [&](float z) {
-            const float x = z - t;
-            if (ri == 2) {  // alpha = 3/2: branch-free
-                const float y = fmaxf(x, 0.f);
-                s0 = fmaf(y, y, s0);
-                s1 += y;
-            } else if (x > 0.f) {
-                const float y = ri == 1 ? 1.f : pos_pow(x, r - 1.f, rim1);
-                s0 = fmaf(x, y, s0);
-                s1 += y;
-            }
-        };
-        for_each(add, first, stride);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s0 += __shfl_xor_sync(FULL, s0, o);
-            s1 += __shfl_xor_sync(FULL, s1, o);
-        }
-        float S0 = s0, S1 = s1;
-        if (!per_warp) {
-            if (lane == 0) {
-                red[it & 1][warp][0] = s0;
-                red[it & 1][warp][1] = s1;
-            }
-            __syncthreads();
-            S0 = 0.f;
-            S1 = 0.f;
-#pragma unroll
-            for (int ww = 0; ww < TAU_NW; ++ww) {
-                S0 += red[it & 1][ww][0];
-                S1 += red[it & 1][ww][1];
-            }
-        }
-        if (!(S1 > 0.f)) break;  // no weight right of t (t at the top already)
-        // r >= 1: t' = t + (S0 - S0^(1-1/r)) / S1;  r < 1: t' = t + (S0 - 1) / (r S1)
-        float step;
-        if (ri == 2) step = (S0 - sqrtf(S0)) / S1;
-        else if (ri == 1) step = (S0 - 1.f) / S1;
-        else if (r >= 1.f) step = (S0 - powf(S0, 1.f - 1.f / r)) / S1;
-        else step = (S0 - 1.f) / (r * S1);
-        const float tn = fminf(hi, fmaxf(lo, t + step));
-        const bool done = !(fabsf(tn - t) > tol);
-        t = tn;
-        if (done) break;
-    }
-    if (per_warp) {
-        __syncthreads();  // every warp is past the caller's earlier use of red
-        if (threadIdx.x == 0) red[0][0][0] = t;
-        __syncthreads();
-        t = red[0][0][0];
-    }
-    return t;
-}
-
 // Exact threshold and (GATHER) the weighted sum of the support's value rows.
 template <int D, bool GATHER>
 __global__ void __launch_bounds__(TAU_NT, D == 64 ? 4 : 3) tau_pv_kernel(const __grid_constant__ DecodeArgs a, int dense, int zcap) {
@@ -1061,13 +982,13 @@ __global__ void __launch_bounds__(TAU_NT, D == 64 ? 4 : 3) tau_pv_kernel(const _
         const float hi = zmax - powf((float)(onchip ? nc : n_tok), 1.f - a.alpha);
         if (nc > 1 && hi > lo) {
             if (onchip) {
-                tau = entmax_tau([&](auto add, int f, int st) { for (int c = f; c < nc; c += st) add(cz[c]); }, nc,
+                tau = entmax_tau<TAU_NT>([&](auto add, int f, int st) { for (int c = f; c < nc; c += st) add(cz[c]); }, nc,
                                  lo, hi, zmax, r, ri, red);
             } else {
                 // too many candidates to hold: stream the z row through shared
                 // memory in coalesced chunks of zcap
                 // (n_tok > zcap >= 1024 here: the block-wide form)
-                tau = entmax_tau(
+                tau = entmax_tau<TAU_NT>(
                     [&](auto add, int f, int st) {
                         for (int c0 = 0; c0 < n_tok; c0 += zcap) {
                             const int m = min(zcap, n_tok - c0);
@@ -1237,7 +1158,7 @@ __global__ void __launch_bounds__(TAU_NT) threshold_kernel(const __grid_constant
     const float lo = zmax - 1.f, hi = zmax - powf((float)n, 1.f - a.alpha);
     float tau = lo;
     if (n > 1 && hi > lo)
-        tau = entmax_tau([&](auto add, int f, int st) { for (int c = f; c < n; c += st) add(tz[c]); }, n, lo, hi,
+        tau = entmax_tau<TAU_NT>([&](auto add, int f, int st) { for (int c = f; c < n; c += st) add(tz[c]); }, n, lo, hi,
                          zmax, r, a.r_int, red);
     if (threadIdx.x == 0) a.tau[bh] = tau;
 }
@@ -1800,6 +1721,9 @@ int decode_sparse_kernels(const DecodeArgs &a) {
         }
     }
     return -1;
+}
+cudaError_t launch_union_list(const DecodeArgs &a, cudaStream_t st) {
+    return launch_pdl(union_kernel, dim3(a.B * a.nk), dim3(UTH), 0, st, a);
 }
 cudaError_t launch_decode_step_tail(const DecodeArgs &a, cudaStream_t st) { EKV_DISPATCH(step_tail_t, a, st); }
 int decode_step_tail_kernels(const DecodeArgs &a) { return a.Hq / a.Hkv > 1 ? 3 : 2; }

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/entmaxkv.h"
+
 namespace ekv {
 
 // Most split-K slots a decode call may use per (sequence, head).
@@ -16,6 +18,14 @@ struct DevInfo {
     int sms;
     int *status;  // device address of the status word
 };
+
+// Argument checks and device queries shared by the C entry points (api.cu).
+int device_info(DevInfo *out);               // current device; ENTMAXKV_* code
+int check_shape(const entmaxkv_shape *s);    // ENTMAXKV_* code
+void kv_range(const entmaxkv_shape *s, int *kv0, int *nk);
+int integer_r(float alpha);                  // 1/(alpha-1) when an integer in 1..8, else 0
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+constexpr int MAX_SEL_PAGES = 196608;        // longest page-table row of a selection
 
 // Grid index -> (sequence, kv head) of a kv-head range [kv0, kv0 + nk), and
 // -> (sequence, query head) of a query-head range [h0, h0 + nh).
@@ -150,6 +160,10 @@ int decode_sparse_kernels(const DecodeArgs &a);  // launches of one launch_decod
 cudaError_t launch_decode_sparse_begin(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_sparse_candidates(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_decode_sparse_finish(const DecodeArgs &a, cudaStream_t st);
+// The union of each group's selections alone, as the sparse paths' first
+// launch: fills ws.union_e / union_blk / union_cnt (and resets ws.zmax and
+// ws.counters) from sel and cnt.
+cudaError_t launch_union_list(const DecodeArgs &a, cudaStream_t st);
 // The decode of a step whose selection marked the union (G > 1: union_map_kernel
 // compacts the marks) or wrote it (G = 1): then q.K and tau with p.V
 cudaError_t launch_decode_step_tail(const DecodeArgs &a, cudaStream_t st);
