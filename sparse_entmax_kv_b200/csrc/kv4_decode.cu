@@ -3,25 +3,37 @@
 //
 // Mathematics.  With k_tj = s_tg c_tj + lo_tg for the coordinates j of group
 // g, the score of token t is
-//   q.k_t = sum_g [ s_tg sum_{j in g} q_j c_tj  +  lo_tg sum_{j in g} q_j ],
-// so the codes themselves are the tensor-core operand: a code in the top
-// mantissa bits of a bf16 with exponent 4 is the number 16 + c, exact, made
-// by one shift and one mask for two codes; the 16 moves into the offset
-// (lo - 16 s).  The products with the bf16 query are exact and are summed in
-// fp32.  The values are treated the same way: the weights p_t s_tg (in three
-// bf16 parts, 24 bits together) multiply 16 + c, and sum_t p_t (lo_tg - 16
-// s_tg) is added at the end.
+//   q.k_t = sum_g [ s_tg sum_{j in g} q_j (c_tj - 7.5) + (lo_tg + 7.5 s_tg) sum_{j in g} q_j ],
+// so the centred codes themselves are the tensor-core operand.  They are
+// centred because the tensor core truncates its fp32 sums: an offset common
+// to all codes would be summed, truncated and cancelled again (with 16 + c
+// as the operand the softmax of 32k tokens was 5e-4 off, relatively).
+//   keys    2 c - 15 is +-(2 m + 1), m < 8: sign and m are stored so that one
+//           rotation and one mask leave the bf16 subnormal +-(2 m + 1) 2^-130;
+//           the query is scaled by a power of two per head, which is exact
+//           and keeps the products normal
+//   values  a code in the top mantissa bits of a bf16 with exponent 4 is 16 +
+//           c; a packed subtraction makes it c - 7.5, exactly.  The weights
+//           p_t s_tg go in as three bf16 parts (24 bits together) and sum_t
+//           p_t (lo_tg + 7.5 s_tg) is added at the end.  Groups of four heads
+//           or fewer put the parts in the columns their heads leave free.
+//           The sums move to a second set of fp32 registers every four tiles,
+//           so that few truncations meet a large sum.
 //
-// Every warp owns a run of 16-token tiles of its group's page list and reads
-// each tile once for all query heads of the group (heads are the n dimension
-// of m16n8k16, tokens or value coordinates the m dimension).
-//   softmax  running max, sum and output per head, one partial a CTA, merged
-//            by combine_kernel in split order
+// The tiles (16 tokens of one kv head) of all groups' page lists form one
+// range that is cut evenly among the warps of a grid that fills the GPU once:
+// ragged batches and any number of groups keep every SM busy to the end.  A
+// warp takes its tiles through a ring of its own in shared memory, filled by
+// bulk copies several tiles ahead, and reads each tile once for all query
+// heads of the group (heads are the n dimension of m16n8k16, tokens or value
+// coordinates the m dimension).
+//   softmax  running max, sum and output per head, one partial for each warp
+//            and group, merged by combine_kernel in token order
 //   entmax   scan_kernel keeps the tokens whose z can still carry weight
-//            (z > running max - 1: no weight exceeds 1) as a list of (z,
-//            value row) per warp; tau_kernel, one CTA a head, drops those
-//            below the head's max - 1, solves for tau and sums p v over the
-//            support
+//            (z > max so far - 1: no weight exceeds 1) as a list of (z, value
+//            row) for each warp and group; tau_kernel, one CTA a head, drops
+//            those below the head's max - 1, solves for tau and sums p v over
+//            the support
 #include <cmath>
 #include <cstring>
 
@@ -35,8 +47,12 @@ namespace {
 
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
-constexpr int AT_SPLIT_CTAS = 148 * 6;  // CTAs the grid aims at
-constexpr int AT_MIN_TILES = 4;         // tiles a warp gets at least
+constexpr int AT_RING = 9216;           // bytes of a warp's ring
+constexpr int AT_MAX_WARPS = 148 * 5 * AT_WARPS;
+constexpr int AT_MIN_TILES = 2;         // tiles a warp gets at least ...
+constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
+constexpr int AT_FLUSH = 4;             // tiles between flushes of the output sums
+constexpr float AT_SLACK = 6.f;         // how far (in powers of two) a score may exceed the reference max
 
 struct Kv4DecodeArgs {
     const uint16_t *q;
@@ -44,77 +60,325 @@ struct Kv4DecodeArgs {
     const int *page_table, *seq_lens;
     const int *union_e, *union_blk, *union_cnt;  // null: every page
     float *out, *tau_out;
-    float *part;          // [S][B Hq][d + 2] softmax partials
+    float *part_o;        // [slots][G][d] softmax partials
+    float2 *part_ml;      // [slots][G]
     float *cand_z;        // [B Hq][max_pages P]
     unsigned *cand_row;   // [B Hq][max_pages P]  blk P + slot
-    int *seg_n;           // [B Hq][seg_len]
-    float *seg_max;       // [B Hq][seg_len]
-    int seg_len;          // segments of a head at most (any kv-head range)
-    int B, Hq, Hkv, P, max_pages, num_blocks, S;
+    int2 *seg;            // [slots][G] candidates of a warp's share of a group, their max
+    int *zmax;            // [B Hq] running max of a head's z (order-mapped), null: none kept
+    int W;                // warps that share the tiles at most
+    int B, Hq, Hkv, P, lp, max_pages, num_blocks;
     int kv0, nk;
     float alpha;
     int r_int;
     int *status;
 };
 
-// (16 + code) of code pair p (bits 4p.. of each half of the unrotated word) as
-// two bf16: the stored word holds pair 0 at the top of the mantissas already.
-template <int p>
-__device__ __forceinline__ unsigned codes_bf16(unsigned w) {
-    const unsigned x = p == 0 ? w : p == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * p);
-    return (x & 0x00780078u) | 0x41804180u;
+// --------------------------------------------------------------- the range of tiles
+
+// Entries of the range: the sequences (nk groups each), or the groups of the
+// selections' unions.
+__device__ __forceinline__ int n_entries(const Kv4DecodeArgs &a) { return a.union_e ? a.B * a.nk : a.B; }
+__device__ __forceinline__ int tokens_of(const Kv4DecodeArgs &a, int b) {
+    const int s = __ldg(a.seq_lens + b), cap = a.max_pages * a.P;
+    return s < 0 ? 0 : min(s, cap);
 }
+// Tiles of each group of entry i.
+__device__ __forceinline__ int entry_tiles(const Kv4DecodeArgs &a, int i) {
+    if (!a.union_e) return n_pages_of(tokens_of(a, i), a.P) << a.lp;
+    int b, kvh;
+    group_of(i, a.kv0, a.nk, b, kvh);
+    return __ldg(a.union_cnt + b * a.Hkv + kvh) << a.lp;
+}
+__device__ __forceinline__ int groups_of_entry(const Kv4DecodeArgs &a) { return a.union_e ? 1 : a.nk; }
+
+// Tiles before the entries of each thread of the CTA (thread i owns entries
+// i C .. i C + C - 1), and their total.
+template <int NT>
+struct Plan {
+    long long pre[NT + 1];
+    long long warp_sum[NT / 32];
+    __device__ void make(const Kv4DecodeArgs &a) {
+        const int n = n_entries(a), C = (n + NT - 1) / NT, m = groups_of_entry(a);
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        long long v = 0;
+        for (int i = threadIdx.x * C; i < min(n, (int)(threadIdx.x + 1) * C); ++i) v += (long long)entry_tiles(a, i) * m;
+        long long x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sum[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += warp_sum[w];
+        pre[threadIdx.x] = x - v;
+        if (threadIdx.x == NT - 1) pre[NT] = x;
+        __syncthreads();
+    }
+    __device__ long long total() const { return pre[NT]; }
+    // Warps that share the range: no more than its tiles, so that none is left without.
+    __device__ int warps(const Kv4DecodeArgs &a) const { return (int)min((long long)a.W, total()); }
+    __device__ long long first_of(const Kv4DecodeArgs &a, int w) const { return total() * w / warps(a); }
+    // First tile of entry i.
+    __device__ long long start_of(const Kv4DecodeArgs &a, int i) const {
+        const int C = (n_entries(a) + NT - 1) / NT, m = groups_of_entry(a);
+        long long s = pre[i / C];
+        for (int k = i / C * C; k < i; ++k) s += (long long)entry_tiles(a, k) * m;
+        return s;
+    }
+};
+
+// One warp's share of one group's list.
+struct Share {
+    int b, kvh, bk, g;  // g: group in the order of the range
+    int U, seq;         // pages of the list, tokens of the sequence
+    int first, last;    // tiles [first, last) of the list
+};
+
+// Walks the entries from tile t on.
+struct Walk {
+    int i;            // entry
+    int T;            // tiles of each of its groups
+    long long start;  // its first tile
+    template <int NT>
+    __device__ void to(const Kv4DecodeArgs &a, const Plan<NT> &p, long long t) {
+        int lo = 0, hi = NT - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.pre[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        start = p.pre[lo];
+        i = lo * ((n_entries(a) + NT - 1) / NT);
+        T = entry_tiles(a, i);
+    }
+    __device__ Share share(const Kv4DecodeArgs &a, long long t, long long end) {
+        const int m = groups_of_entry(a);
+        while (start + (long long)T * m <= t) {
+            start += (long long)T * m;
+            T = entry_tiles(a, ++i);
+        }
+        const int sub = (int)((t - start) / T);
+        Share s;
+        s.g = i * m + sub;
+        group_of(s.g, a.kv0, a.nk, s.b, s.kvh);
+        s.bk = s.b * a.Hkv + s.kvh;
+        s.U = T >> a.lp;
+        s.seq = tokens_of(a, s.b);
+        const long long at = start + (long long)sub * T;
+        s.first = (int)(t - at);
+        s.last = (int)min((long long)T, s.first + (end - t));
+        return s;
+    }
+};
+
+// Where the warps' shares of one group lie: slots w + g for w0 <= w <= w1
+// (w and g both ascend along the range, so no two shares meet in a slot).
+struct GroupSlots {
+    long long start;
+    int w0, w1, g;
+};
+template <int NT>
+__device__ GroupSlots group_slots(const Kv4DecodeArgs &a, const Plan<NT> &p, int b, int kvh) {
+    GroupSlots r;
+    r.g = b * a.nk + kvh - a.kv0;
+    const int i = a.union_e ? r.g : b;
+    const int T = entry_tiles(a, i);
+    r.w0 = 0;
+    r.w1 = -1;
+    if (T == 0) return r;
+    r.start = p.start_of(a, i) + (a.union_e ? 0 : (long long)(kvh - a.kv0) * T);
+    const long long W = p.warps(a), total = p.total();
+    r.w0 = (int)(((r.start + 1) * W - 1) / total);
+    r.w1 = (int)(((r.start + T) * W - 1) / total);
+    return r;
+}
+// The first slot of a call: every kv head has its own, for as many warps as a
+// call on it alone may use, so calls on disjoint ranges share a workspace.
+__host__ __device__ inline size_t slots_per_head(int B) { return (size_t)AT_MAX_WARPS + B; }
+
+// --------------------------------------------------------------- the ring of tiles
+
+// A stage: the key tile (and the value tile), and what it holds.
+template <int D, bool BOTH>
+struct TileRing {
+    static constexpr int STAGE = Kv4<D>::TILE * (BOTH ? 2 : 1);
+    static constexpr int NST = AT_RING / STAGE > 8 ? 8 : AT_RING / STAGE;  // a power of two: 4 or 8
+    static_assert((NST & (NST - 1)) == 0, "stages");
+    unsigned char *base;
+    uint64_t *bar;
+    int4 *info;  // block (-1: nothing to read), valid tokens, head mask, tile of the page
+    unsigned issued = 0, taken = 0;
+    int e0 = 0, ent = 0, blk = 0;  // the lane's entry of 32 list entries from e0 on
+
+    __device__ __forceinline__ void init(unsigned char *b, uint64_t *bars, int4 *i) {
+        base = b;
+        bar = bars;
+        info = i;
+        if ((threadIdx.x & 31) == 0) {
+            for (int s = 0; s < NST; ++s) mbar_init(&bar[s], 1);
+            mbar_fence_init();
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void start() { e0 = -(1 << 30); }  // a new list
+    __device__ __forceinline__ void issue(const Kv4DecodeArgs &a, const Share &s, int tile) {
+        const int lane = threadIdx.x & 31;
+        const int e = tile >> a.lp;
+        if (e - e0 >= 32 || e < e0) {
+            e0 = e;
+            const int i = e + lane;
+            ent = 0;
+            blk = -1;
+            if (i < s.U) {
+                if (a.union_e) {
+                    ent = __ldg(a.union_e + (size_t)s.bk * a.max_pages + i);
+                    blk = __ldg(a.union_blk + (size_t)s.bk * a.max_pages + i);
+                } else {
+                    blk = __ldg(a.page_table + (size_t)s.b * a.max_pages + i);
+                    if (blk < 0 || blk >= a.num_blocks) {
+                        atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
+                        blk = -1;
+                    }
+                }
+            }
+        }
+        const int en = __shfl_sync(FULL, ent, e - e0), bl = __shfl_sync(FULL, blk, e - e0);
+        const int st = issued++ % NST;
+        if (lane == 0) {
+            const int t16 = tile & ((1 << a.lp) - 1);
+            const int nval = min(16, s.seq - (a.union_e ? en >> 8 : e) * a.P - 16 * t16);
+            const bool has = bl >= 0 && nval > 0;
+            info[st] = make_int4(has ? bl : -1, nval, a.union_e ? en & 0xff : 0xff, t16);
+            if (has) {
+                const size_t at = kv4_tile<D>(bl, a.Hkv, s.kvh, a.P, t16);
+                mbar_arrive_expect_tx(&bar[st], STAGE);
+                bulk_g2s(base + st * STAGE, a.k4 + at, Kv4<D>::TILE, &bar[st]);
+                if (BOTH) bulk_g2s(base + st * STAGE + Kv4<D>::TILE, a.v4 + at, Kv4<D>::TILE, &bar[st]);
+            } else {
+                mbar_arrive(&bar[st]);
+            }
+        }
+    }
+    // Waits for the next stage.  False: it did not come (the status word says so).
+    __device__ __forceinline__ bool take(const Kv4DecodeArgs &a, int4 &what, unsigned char *&tile) {
+        const int st = taken % NST;
+        const bool ok = mbar_wait(&bar[st], (taken / NST) & 1, a.status);
+        ++taken;
+        what = info[st];
+        tile = base + st * STAGE;
+        return __all_sync(FULL, ok);
+    }
+    // After a wait that ran out: the copies in flight have to land before the CTA ends.
+    __device__ void drain(const Kv4DecodeArgs &a) {
+        for (; taken < issued; ++taken) mbar_wait(&bar[taken % NST], (taken / NST) & 1, a.status);
+    }
+};
+
+// --------------------------------------------------------------- operands
+
+// (2 c - 15) 2^-130 of pair p of a key word, as two bf16.
+template <int p>
+__device__ __forceinline__ unsigned key_bf16(unsigned w) {
+    return ((p ? __funnelshift_r(w, w, 4 * p) : w) & 0x80708070u) | 0x00080008u;
+}
+// c - 7.5 of pair p of a value word, as two bf16: 16 + c less 23.5.
+template <int p>
+__device__ __forceinline__ unsigned value_bf16(unsigned w) {
+    const unsigned x = (((p == 0 ? w : p == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * p)) & 0x00780078u) | 0x41804180u);
+    unsigned y;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3f803f80u), "r"(0xc1bcc1bcu));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The top halves of x0 and x1.
+__device__ __forceinline__ unsigned top_halves(float x0, float x1) {
+    return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+}
+__device__ __forceinline__ float below_top(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
 template <int N>
 __device__ __forceinline__ void load_words(const unsigned char *src, unsigned (&w)[N]) {
     if constexpr (N == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
+        const uint4 v = *reinterpret_cast<const uint4 *>(src);
         w[0] = v.x;
         w[1] = v.y;
         w[2] = v.z;
         w[3] = v.w;
     } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+        const uint2 v = *reinterpret_cast<const uint2 *>(src);
         w[0] = v.x;
         w[1] = v.y;
     }
 }
 
-// The group's queries as B fragments (lane: head lane / 4), and the sums of
-// each coordinate group for the two heads of the lane's accumulator columns.
-template <int D>
+// The group's queries as B fragments: column n holds head n % CP, scaled by
+// a power of two 2^e of its own; for the lane's two accumulator columns the
+// sums of each coordinate group, in the units of the products, and the factor
+// from those units to z.
+template <int D, int CP>
 struct Queries {
+    static constexpr int NE = CP == 1 ? 1 : 2;  // distinct columns of a lane
     unsigned b[D / 16][2];
-    float sum[Kv4<D>::NG][2];
-    __device__ __forceinline__ void load(const uint16_t *q, int G) {
-        const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-        const unsigned *qw = reinterpret_cast<const unsigned *>(q + (size_t)r * D);
+    float sum[Kv4<D>::NG][NE];
+    float factor[NE];
+    __device__ __forceinline__ void load(const uint16_t *q, int G, float scale) {
+        const int lane = threadIdx.x & 31, h = (lane >> 2) % CP, c = lane & 3;
+        const unsigned *qw = reinterpret_cast<const unsigned *>(q + (size_t)h * D);
+        float t[Kv4<D>::NG];
+        unsigned top = 0;
 #pragma unroll
         for (int g = 0; g < Kv4<D>::NG; ++g) {
-            float t = 0.f;
+            t[g] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j0 = 64 * g + 16 * c + 8 * i + 4 * h;
-                    unsigned *d = b[2 * (2 * g + i) + h];
-                    d[0] = r < G ? qw[j0 / 2] : 0u;
-                    d[1] = r < G ? qw[j0 / 2 + 1] : 0u;
-                    t += (bf16lo(d[0]) + bf16hi(d[0])) + (bf16lo(d[1]) + bf16hi(d[1]));
+                for (int k = 0; k < 2; ++k) {
+                    const int j0 = 64 * g + 16 * c + 8 * i + 4 * k;
+                    unsigned *d = b[2 * (2 * g + i) + k];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        d[x] = h < G ? qw[j0 / 2 + x] : 0u;
+                        t[g] += bf16lo(d[x]) + bf16hi(d[x]);
+                        top = max(top, max((d[x] >> 7) & 0xffu, (d[x] >> 23) & 0xffu));  // exponent fields
+                    }
                 }
-            t += __shfl_xor_sync(FULL, t, 1);
-            t += __shfl_xor_sync(FULL, t, 2);
-            sum[g][0] = __shfl_sync(FULL, t, 8 * c);
-            sum[g][1] = __shfl_sync(FULL, t, 8 * c + 4);
+            t[g] += __shfl_xor_sync(FULL, t[g], 1);
+            t[g] += __shfl_xor_sync(FULL, t[g], 2);
+        }
+        top = max(top, __shfl_xor_sync(FULL, top, 1));
+        top = max(top, __shfl_xor_sync(FULL, top, 2));
+        // the largest |q| goes to about 2^120: products with the subnormal
+        // codes stay normal down to 2^-110 of it, scaled sums below 2^127, and
+        // the factor below stays a normal number
+        const int E = max((int)top - 127, 0);
+        const int e = max(0, min(max(120 - E, 9), 127 - E));
+        const float up = __uint_as_float((unsigned)(e + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) b[i][x] = top_halves(bf16lo(b[i][x]) * up, bf16hi(b[i][x]) * up);
+#pragma unroll
+        for (int v = 0; v < NE; ++v) {
+            const int src = 4 * (2 * c + v);
+            const int ec = __shfl_sync(FULL, e, src);
+            factor[v] = ldexpf(scale, 129 - ec);
+#pragma unroll
+            for (int g = 0; g < Kv4<D>::NG; ++g) sum[g][v] = ldexpf(__shfl_sync(FULL, t[g], src), ec - 129);
         }
     }
 };
 
-// q.k of the 16 tokens of a tile: z[0], z[1] token lane / 4, heads 2 (lane % 4)
-// and + 1; z[2], z[3] token lane / 4 + 8.
-template <int D>
-__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D> &Q, float scale, float (&z)[4]) {
-    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL;
+// z of the 16 tokens of a tile: z[e] token lane / 4, z[2 + e] token lane / 4 +
+// 8, columns 2 (lane % 4) + e.
+template <int D, int CP>
+__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D, CP> &Q, float (&z)[4]) {
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, NE = Queries<D, CP>::NE;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     unsigned w0[WPL], w1[WPL];
     load_words<WPL>(tile + r * (D / 2) + c * (4 * WPL), w0);
@@ -123,8 +387,8 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
     unsigned p0[NG], p1[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        p0[g] = __ldg(pp + r * NG + g);
-        p1[g] = __ldg(pp + (r + 8) * NG + g);
+        p0[g] = pp[r * NG + g];
+        p1[g] = pp[(r + 8) * NG + g];
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) z[v] = 0.f;
@@ -133,331 +397,451 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 2 * g; i < 2 * g + 2; ++i) {
-            mma_bf16_16816(acc, codes_bf16<0>(w0[i]), codes_bf16<0>(w1[i]), codes_bf16<1>(w0[i]),
-                           codes_bf16<1>(w1[i]), Q.b[2 * i][0], Q.b[2 * i][1]);
-            mma_bf16_16816(acc, codes_bf16<2>(w0[i]), codes_bf16<2>(w1[i]), codes_bf16<3>(w0[i]),
-                           codes_bf16<3>(w1[i]), Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
+            mma_bf16_16816(acc, key_bf16<0>(w0[i]), key_bf16<0>(w1[i]), key_bf16<1>(w0[i]), key_bf16<1>(w1[i]),
+                           Q.b[2 * i][0], Q.b[2 * i][1]);
+            mma_bf16_16816(acc, key_bf16<2>(w0[i]), key_bf16<2>(w1[i]), key_bf16<3>(w0[i]), key_bf16<3>(w1[i]),
+                           Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
         }
         const float s0 = bf16lo(p0[g]), s1 = bf16lo(p1[g]);
-        const float o0 = fmaf(-16.f, s0, bf16hi(p0[g])), o1 = fmaf(-16.f, s1, bf16hi(p1[g]));
-        z[0] = fmaf(s0, acc[0], fmaf(o0, Q.sum[g][0], z[0]));
-        z[1] = fmaf(s0, acc[1], fmaf(o0, Q.sum[g][1], z[1]));
-        z[2] = fmaf(s1, acc[2], fmaf(o1, Q.sum[g][0], z[2]));
-        z[3] = fmaf(s1, acc[3], fmaf(o1, Q.sum[g][1], z[3]));
-    }
+        const float o0 = fmaf(7.5f, s0, bf16hi(p0[g])), o1 = fmaf(7.5f, s1, bf16hi(p1[g]));
 #pragma unroll
-    for (int v = 0; v < 4; ++v) z[v] *= scale;
-}
-
-// The page list of a group and the tiles of one warp of one CTA.
-struct Span {
-    int b, kvh, bk, U, seq;
-    int first, last;  // tiles [first, last) of the list
-};
-
-__device__ __forceinline__ Span warp_span(const Kv4DecodeArgs &a, int group, int seg) {
-    Span s;
-    group_of(group, a.kv0, a.nk, s.b, s.kvh);
-    s.bk = s.b * a.Hkv + s.kvh;
-    s.seq = seq_len_of(a.seq_lens, s.b, a.P, a.max_pages, a.status);
-    s.U = a.union_e ? a.union_cnt[s.bk] : n_pages_of(s.seq, a.P);
-    const long long T = (long long)s.U * (a.P / 16);
-    const int W = a.S * AT_WARPS;
-    s.first = (int)(T * seg / W);
-    s.last = (int)(T * (seg + 1) / W);
-    return s;
-}
-
-// Tile `t` of the list: its page's block (-1: skip), valid tokens and heads.
-struct TileAt {
-    int blk, t16, nval, mask;
-};
-__device__ __forceinline__ TileAt tile_at(const Kv4DecodeArgs &a, const Span &s, int t) {
-    const int per = a.P / 16;
-    const int e = t / per;
-    TileAt r;
-    r.t16 = t - e * per;
-    int page;
-    if (a.union_e) {
-        const int entry = __ldg(a.union_e + (size_t)s.bk * a.max_pages + e);
-        r.blk = __ldg(a.union_blk + (size_t)s.bk * a.max_pages + e);
-        page = entry >> 8;
-        r.mask = entry & 0xff;
-    } else {
-        r.blk = __ldg(a.page_table + (size_t)s.b * a.max_pages + e);
-        page = e;
-        r.mask = 0xff;
-        if (r.blk < 0 || r.blk >= a.num_blocks) {
-            atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
-            r.blk = -1;
+        for (int e = 0; e < NE; ++e) {
+            z[e] = fmaf(s0, acc[e], fmaf(o0, Q.sum[g][e], z[e]));
+            z[2 + e] = fmaf(s1, acc[2 + e], fmaf(o1, Q.sum[g][e], z[2 + e]));
         }
     }
-    r.nval = max(0, min(16, s.seq - page * a.P - 16 * r.t16));
-    if (r.nval == 0) r.blk = -1;
-    return r;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+        z[e] *= Q.factor[e];
+        z[2 + e] *= Q.factor[e];
+    }
+}
+// Tokens behind the sequence and heads that did not select the page: -inf.
+template <int CP>
+__device__ __forceinline__ void mask_scores(const int4 &what, int G, float (&z)[4]) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int heads = (1 << G) - 1;
+    const int mask = what.z & heads;
+    if (what.y >= 16 && mask == (1 << CP) - 1) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (r + 8 * (v >> 1) >= what.y || !((mask >> ((2 * c + (v & 1)) % CP)) & 1)) z[v] = -INFINITY;
 }
 
 // -------------------------------------------------------------- softmax
 
-template <int D>
-struct __align__(16) SoftmaxShared {
-    float o[AT_WARPS][8][D];
-    float m[AT_WARPS][8], l[AT_WARPS][8];
-};
-
-template <int D>
-__global__ void __launch_bounds__(AT_THREADS) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+template <int D, int CP>
+__global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
-    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16;
-    __shared__ SoftmaxShared<D> sh;
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, CP>::NE;
+    using Ring = TileRing<D, true>;
+    extern __shared__ __align__(128) unsigned char rings[];
+    __shared__ uint64_t bars[AT_WARPS][Ring::NST];
+    __shared__ int4 infos[AT_WARPS][Ring::NST];
+    __shared__ Plan<AT_THREADS> plan;
+    plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    const int group = blockIdx.x / a.S, split = blockIdx.x % a.S;
+    const int w = blockIdx.x * AT_WARPS + warp;
+    if (w >= plan.warps(a)) return;
     const int G = a.Hq / a.Hkv;
-    const Span sp = warp_span(a, group, split * AT_WARPS + warp);
-    Queries<D> Q;
-    Q.load(a.q + ((size_t)sp.b * a.Hq + sp.kvh * G) * D, G);
-    const float scale = 1.4426950408889634f * rsqrtf((float)D);  // z in powers of two
+    const int part = r / CP;  // the part of the weights that column r carries
+    Ring ring;
+    ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
+    long long t = plan.first_of(a, w);
+    const long long end = plan.first_of(a, w + 1);
+    Walk walk;
+    walk.to(a, plan, t);
+    while (t < end) {
+        const Share sh = walk.share(a, t, end);
+        t += sh.last - sh.first;
+        ring.start();
+        for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        Queries<D, CP> Q;
+        // z in powers of two
+        Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, G, 1.4426950408889634f * rsqrtf((float)D));
 
-    float acc[MT][4];
+        float acc[MT][4], tot[MT][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][v] = 0.f;
-    float off[NG] = {};                     // head r: sum p (lo - 16 s), this lane's tokens
-    float m[2] = {-INFINITY, -INFINITY};    // heads 2c, 2c + 1
-    float l[2] = {0.f, 0.f};
-    for (int t = sp.first; t < sp.last; ++t) {
-        const TileAt ta = tile_at(a, sp, t);
-        if (ta.blk < 0) continue;
-        const size_t at = kv4_tile<D>(ta.blk, a.Hkv, sp.kvh, a.P, ta.t16);
-        float z[4];
-        tile_scores<D>(a.k4 + at, Q, scale, z);
-        const int mask = ta.mask & ((1 << G) - 1);
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            if (r + 8 * (v >> 1) >= ta.nval || !((mask >> (2 * c + (v & 1))) & 1)) z[v] = -INFINITY;
-        float corr[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float tm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
-            const float mn = fmaxf(m[e], tm);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            corr[e] = exp2f(m[e] - base);
-            m[e] = mn;
-            z[e] = exp2f(z[e] - base);
-            z[2 + e] = exp2f(z[2 + e] - base);
-            l[e] = fmaf(l[e], corr[e], z[e] + z[2 + e]);
-        }
-        if (__any_sync(FULL, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][v] *= corr[v & 1];
-            const float c0 = __shfl_sync(FULL, corr[0], r >> 1), c1 = __shfl_sync(FULL, corr[1], r >> 1);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) off[g] *= (r & 1) ? c1 : c0;
-        }
-        // weights of head r, tokens 2c, 2c + 1, 2c + 8, 2c + 9
-        float p[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int src = 4 * (2 * c + u) + (r >> 1);
-            const float x0 = __shfl_sync(FULL, z[0], src), x1 = __shfl_sync(FULL, z[1], src);
-            const float y0 = __shfl_sync(FULL, z[2], src), y1 = __shfl_sync(FULL, z[3], src);
-            p[u] = (r & 1) ? x1 : x0;
-            p[2 + u] = (r & 1) ? y1 : y0;
-        }
-        const unsigned char *vt = a.v4 + at;
-        unsigned w0[WPL], w1[WPL];
-        const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
-        load_words<WPL>(vt + c * D + piece, w0);
-        load_words<WPL>(vt + (c + 4) * D + piece, w1);
-        const unsigned *vp = reinterpret_cast<const unsigned *>(vt + Kv4<D>::CODES);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int tok = 2 * c + (u & 1) + 8 * (u >> 1);
-                // rows behind the sequence, and rows of pages that head r did not
-                // select, count as zero whatever they hold
-                const unsigned pr = tok < ta.nval && ((mask >> r) & 1) ? __ldg(vp + tok * NG + g) : 0u;
-                const float s = bf16lo(pr);
-                off[g] = fmaf(p[u], fmaf(-16.f, s, bf16hi(pr)), off[g]);
-                x[u] = p[u] * s;
+            for (int v = 0; v < 4; ++v) acc[i][v] = tot[i][v] = 0.f;
+        float off[NG] = {};                 // head of column r: sum p (lo + 7.5 s), this lane's tokens
+        float m[2] = {-INFINITY, -INFINITY};  // reference max of the lane's columns
+        float l[2] = {0.f, 0.f};
+        for (int i = sh.first; i < sh.last; ++i) {
+            int4 what;
+            unsigned char *tile;
+            if (!ring.take(a, what, tile)) {
+                ring.drain(a);
+                return;
             }
+            if (what.x >= 0) {
+                float z[4];
+                tile_scores<D, CP>(tile, Q, z);
+                mask_scores<CP>(what, G, z);
+                // the reference max follows only when a score passes it by AT_SLACK
+                bool up = false;
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-                const unsigned b0 = (unsigned)f2bf(x[0]) | ((unsigned)f2bf(x[1]) << 16);
-                const unsigned b1 = (unsigned)f2bf(x[2]) | ((unsigned)f2bf(x[3]) << 16);
-                x[0] -= bf16lo(b0);
-                x[1] -= bf16hi(b0);
-                x[2] -= bf16lo(b1);
-                x[3] -= bf16hi(b1);
+                for (int e = 0; e < NE; ++e) up |= !(fmaxf(z[e], z[2 + e]) <= m[e] + AT_SLACK);
+                if (__any_sync(FULL, up)) {
+                    float corr[2] = {1.f, 1.f};
 #pragma unroll
-                for (int i = 2 * g; i < 2 * g + 2; ++i) {
-                    mma_bf16_16816(acc[2 * i], codes_bf16<0>(w0[i]), codes_bf16<1>(w0[i]), codes_bf16<0>(w1[i]),
-                                   codes_bf16<1>(w1[i]), b0, b1);
-                    mma_bf16_16816(acc[2 * i + 1], codes_bf16<2>(w0[i]), codes_bf16<3>(w0[i]), codes_bf16<2>(w1[i]),
-                                   codes_bf16<3>(w1[i]), b0, b1);
+                    for (int e = 0; e < NE; ++e) {
+                        float tm = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
+                        const float mn = fmaxf(m[e], tm);
+                        corr[e] = mn == -INFINITY ? 1.f : exp2f(m[e] - mn);
+                        m[e] = mn;
+                        l[e] *= corr[e];
+                    }
+                    if (NE == 1) corr[1] = corr[0];
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            acc[k][v] *= corr[v & 1];
+                            tot[k][v] *= corr[v & 1];
+                        }
+                    const float c0 = __shfl_sync(FULL, corr[0], r >> 1), c1 = __shfl_sync(FULL, corr[1], r >> 1);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) off[g] *= (r & 1) ? c1 : c0;
+                }
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float base = m[e] == -INFINITY ? 0.f : m[e];
+                    z[e] = ex2(z[e] - base);
+                    z[2 + e] = ex2(z[2 + e] - base);
+                    l[e] += z[e] + z[2 + e];
+                }
+                // weights of column r, tokens 2c, 2c + 1, 2c + 8, 2c + 9
+                float p[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int src = 4 * (2 * c + u) + (r >> 1);
+                    const float x0 = __shfl_sync(FULL, z[0], src), y0 = __shfl_sync(FULL, z[2], src);
+                    if constexpr (NE == 1) {
+                        p[u] = x0;
+                        p[2 + u] = y0;
+                    } else {
+                        const float x1 = __shfl_sync(FULL, z[1], src), y1 = __shfl_sync(FULL, z[3], src);
+                        p[u] = (r & 1) ? x1 : x0;
+                        p[2 + u] = (r & 1) ? y1 : y0;
+                    }
+                }
+                const unsigned char *vt = tile + Kv4<D>::TILE;
+                unsigned w0[WPL], w1[WPL];
+                const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
+                load_words<WPL>(vt + c * D + piece, w0);
+                load_words<WPL>(vt + (c + 4) * D + piece, w1);
+                unsigned pr[4][NG];
+                const unsigned *vp = reinterpret_cast<const unsigned *>(vt + Kv4<D>::CODES);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    unsigned two[2 * NG];
+                    load_words<2 * NG>(reinterpret_cast<const unsigned char *>(vp + (2 * c + 8 * u) * NG), two);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        pr[2 * u][g] = two[g];
+                        pr[2 * u + 1][g] = two[NG + g];
+                    }
+                }
+                // rows behind the sequence, and rows of pages that the head
+                // did not select, count as zero whatever they hold
+                if (what.y < 16 || !((what.z >> (r % CP)) & 1)) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (2 * c + (u & 1) + 8 * (u >> 1) >= what.y || !((what.z >> (r % CP)) & 1))
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) pr[u][g] = 0u;
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float x[4], y[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float s = bf16lo(pr[u][g]);
+                        off[g] = fmaf(p[u], fmaf(7.5f, s, bf16hi(pr[u][g])), off[g]);
+                        x[u] = p[u] * s;
+                        y[u] = below_top(x[u]);
+                    }
+                    // the B fragments: columns of parts 0 and 1 (and 2), then the rest
+                    constexpr int NB = CP == 8 ? 3 : CP == 4 ? 2 : 1;
+                    unsigned bf[NB][2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const unsigned hi = top_halves(x[2 * u], x[2 * u + 1]);
+                        const unsigned mid = top_halves(y[2 * u], y[2 * u + 1]);
+                        const unsigned low = top_halves(below_top(y[2 * u]), below_top(y[2 * u + 1]));
+                        if constexpr (CP == 8) {
+                            bf[0][u] = hi;
+                            bf[NB / 2][u] = mid;
+                            bf[NB - 1][u] = low;
+                        } else if constexpr (CP == 4) {
+                            bf[0][u] = part ? mid : hi;
+                            bf[NB - 1][u] = part ? 0u : low;
+                        } else {
+                            bf[0][u] = part == 0 ? hi : part == 1 ? mid : part == 2 ? low : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 2 * g; k < 2 * g + 2; ++k) {
+                        const unsigned a0 = value_bf16<0>(w0[k]), a1 = value_bf16<1>(w0[k]), a2 = value_bf16<0>(w1[k]),
+                                       a3 = value_bf16<1>(w1[k]);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) mma_bf16_16816(acc[2 * k], a0, a1, a2, a3, bf[n][0], bf[n][1]);
+                        const unsigned d0 = value_bf16<2>(w0[k]), d1 = value_bf16<3>(w0[k]), d2 = value_bf16<2>(w1[k]),
+                                       d3 = value_bf16<3>(w1[k]);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) mma_bf16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[n][0], bf[n][1]);
+                    }
+                }
+                if ((ring.taken & (AT_FLUSH - 1)) == 0) {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            tot[k][v] += acc[k][v];
+                            acc[k][v] = 0.f;
+                        }
                 }
             }
+            __syncwarp();
+            if (i + Ring::NST < sh.last) ring.issue(a, sh, i + Ring::NST);
         }
-    }
-    // the warp's state: sums over the lanes that share a head
+        // the share's partial: sums over the lanes of a column and over the
+        // columns of a head, through the ring's memory (no copy is in flight)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(FULL, l[e], o);
-    if (lane < 4)
+            for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(FULL, l[e], o);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            sh.m[warp][2 * c + e] = m[e];
-            sh.l[warp][2 * c + e] = l[e];
+        for (int g = 0; g < NG; ++g) {
+            off[g] += __shfl_xor_sync(FULL, off[g], 1);
+            off[g] += __shfl_xor_sync(FULL, off[g], 2);
         }
+        const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
+        if (r == 0)
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        off[g] += __shfl_xor_sync(FULL, off[g], 1);
-        off[g] += __shfl_xor_sync(FULL, off[g], 2);
-    }
+            for (int e = 0; e < NE; ++e)
+                if (2 * c + e < min(CP, G)) a.part_ml[slot * G + 2 * c + e] = make_float2(m[e], l[e]);
+        float *stage = reinterpret_cast<float *>(rings + warp * AT_RING);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        // tile mt holds coordinates j (row r) and j + 1 (row r + 8)
-        const int j = 64 * (mt >> 2) + 8 * r + 4 * ((mt >> 1) & 1) + 2 * (mt & 1);
+        for (int k = 0; k < MT; ++k) {
+            // tile k holds coordinates j (row r) and j + 1 (row r + 8)
+            const int j = 64 * (k >> 2) + 8 * r + 4 * ((k >> 1) & 1) + 2 * (k & 1);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const float o = __shfl_sync(FULL, off[mt >> 2], 4 * (2 * c + (v & 1)));
-            sh.o[warp][2 * c + (v & 1)][j + (v >> 1)] = acc[mt][v] + o;
+            for (int v = 0; v < 4; ++v) tot[k][v] += acc[k][v];
+#pragma unroll
+            for (int v = 0; v < 4; v += CP == 1 ? 2 : 1) {
+                float o = tot[k][v];
+                if (CP == 1) o += tot[k][v + 1];
+                if (CP <= 2) o += __shfl_xor_sync(FULL, o, 1);
+                if (CP <= 4) o += __shfl_xor_sync(FULL, o, 2);
+                const int n = 2 * c + (v & 1);
+                o += __shfl_sync(FULL, off[k >> 2], 4 * (n % CP));
+                if (n < min(CP, G)) stage[n * D + j + (v >> 1)] = o;
+            }
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += AT_THREADS) {
-        const int g = i / D, j = i % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < AT_WARPS; ++w) M = fmaxf(M, sh.m[w][g]);
-        float num = 0.f, den = 0.f;
-#pragma unroll
-        for (int w = 0; w < AT_WARPS; ++w) {
-            if (sh.l[w][g] == 0.f) continue;  // no token (NaN scores make it NaN)
-            const float f = exp2f(sh.m[w][g] - M);
-            num = fmaf(f, sh.o[w][g][j], num);
-            den = fmaf(f, sh.l[w][g], den);
-        }
-        float *o = a.part + ((size_t)split * a.B * a.Hq + sp.b * a.Hq + sp.kvh * G + g) * (D + 2);
-        o[2 + j] = num;
-        if (j == 0) {
-            o[0] = M;
-            o[1] = den;
-        }
+        __syncwarp();
+        for (int i = lane; i < G * D / 4; i += 32)
+            reinterpret_cast<float4 *>(a.part_o + slot * G * D)[i] = reinterpret_cast<const float4 *>(stage)[i];
+        // the next share's copies write over the stage
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
     }
 }
 
-// The splits of a head, merged in order.
+constexpr int CB_NT = 256;
+
+// The shares of a head, merged in token order.
 template <int D>
-__global__ void __launch_bounds__(D) kv4_combine_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
-    const int G = a.Hq / a.Hkv, j = threadIdx.x;
+    constexpr int SUB = CB_NT / D;
+    extern __shared__ float weight[];  // of each share
+    __shared__ Plan<CB_NT> plan;
+    __shared__ float red[2][CB_NT / 32];
+    __shared__ float o_sh[SUB][D];
+    const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int b, h;
     head_of(blockIdx.x, a.kv0 * G, a.nk * G, b, h);
     const int bh = b * a.Hq + h;
-    const uint16_t qb = a.q[(size_t)bh * D + j];
+    const uint16_t qb = threadIdx.x < D ? a.q[(size_t)bh * D + threadIdx.x] : (uint16_t)0;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.B; i += CB_NT)
+            if (a.seq_lens[i] > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
+    plan.make(a);
+    const GroupSlots gs = group_slots(a, plan, b, h / G);
+    const int n = gs.w1 - gs.w0 + 1;
+    const size_t slot0 = a.kv0 * slots_per_head(a.B) + gs.w0 + gs.g;
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
-    const size_t step = (size_t)a.B * a.Hq * (D + 2);
-    const float *p = a.part + (size_t)bh * (D + 2);
     float M = -INFINITY;
-    for (int s = 0; s < a.S; ++s) M = fmaxf(M, __ldcg(p + s * step));
-    float num = 0.f, den = 0.f;
-    for (int s = 0; s < a.S; ++s) {
-        const float l = __ldcg(p + s * step + 1);
-        if (l == 0.f) continue;
-        const float f = exp2f(__ldcg(p + s * step) - M);
-        den = fmaf(f, l, den);
-        num = fmaf(f, __ldcg(p + s * step + 2 + j), num);
+    for (int s = threadIdx.x; s < n; s += CB_NT) M = fmaxf(M, __ldcg(&a.part_ml[(slot0 + s) * G + h % G]).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < CB_NT / 32; ++i) M = fmaxf(M, red[0][i]);
+    float den = 0.f;
+    for (int s = threadIdx.x; s < n; s += CB_NT) {
+        const float2 ml = __ldcg(&a.part_ml[(slot0 + s) * G + h % G]);
+        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);  // no token of the head (NaN scores make it NaN)
+        weight[s] = f;
+        den = fmaf(f, ml.y, den);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(FULL, den, o);
+    if (lane == 0) red[1][warp] = den;
+    __syncthreads();
+    den = 0.f;
+#pragma unroll
+    for (int i = 0; i < CB_NT / 32; ++i) den += red[1][i];
+    const int j = threadIdx.x % D, sub = threadIdx.x / D;
+    const float *p = a.part_o + (slot0 * G + h % G) * D + j;
+    float num = 0.f;
+#pragma unroll 8
+    for (int s = sub; s < n; s += SUB) {
+        const float f = weight[s], x = __ldcg(p + (size_t)s * G * D);
+        if (f != 0.f) num = fmaf(f, x, num);
+    }
+    o_sh[sub][j] = num;
+    __syncthreads();
     const float nan = __int_as_float(0x7fc00000);
-    if (!fine && j == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
-    // den is 0 only without tokens (the largest weight of a split is 1); NaN
-    // scores make it NaN
+    if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
+    // den is 0 only without tokens (the largest weight of a share is at least
+    // 1); NaN scores make it NaN
     const bool none = den == 0.f;
-    a.out[(size_t)bh * D + j] = !fine ? nan : none ? 0.f : num / den;
-    if (j == 0 && a.tau_out) a.tau_out[bh] = !fine || none ? nan : 0.6931471805599453f * (M + log2f(den));
+    if (sub == 0) {
+#pragma unroll
+        for (int i = 1; i < SUB; ++i) num += o_sh[i][j];
+        a.out[(size_t)bh * D + j] = !fine ? nan : none ? 0.f : num / den;
+    }
+    if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = !fine || none ? nan : 0.6931471805599453f * (M + log2f(den));
 }
 
 // --------------------------------------------------------------- entmax
 
-template <int D>
-__global__ void __launch_bounds__(AT_THREADS) kv4_scan_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+__global__ void kv4_reset_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    const int group = blockIdx.x / a.S, seg = (blockIdx.x % a.S) * AT_WARPS + warp;
-    const int G = a.Hq / a.Hkv;
-    const Span sp = warp_span(a, group, seg);
-    Queries<D> Q;
-    const int h0 = sp.b * a.Hq + sp.kvh * G;
-    Q.load(a.q + (size_t)h0 * D, G);
-    const float scale = (a.alpha - 1.f) * rsqrtf((float)D);
-    const size_t row_len = (size_t)a.max_pages * a.P;
+    const int G = a.Hq / a.Hkv, i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= a.B * a.nk * G) return;
+    int b, h;
+    head_of(i, a.kv0 * G, a.nk * G, b, h);
+    a.zmax[b * a.Hq + h] = ORD_NEG_INF;
+}
 
-    float m[2] = {-INFINITY, -INFINITY};  // heads 2c, 2c + 1: the warp's max so far
-    int n[8] = {};                        // candidates of each head
-    bool bad[2] = {false, false};         // the lane saw a NaN score
-    for (int t = sp.first; t < sp.last; ++t) {
-        const TileAt ta = tile_at(a, sp, t);
-        if (ta.blk < 0) continue;
-        float z[4];
-        tile_scores<D>(a.k4 + kv4_tile<D>(ta.blk, a.Hkv, sp.kvh, a.P, ta.t16), Q, scale, z);
-        const int mask = ta.mask & ((1 << G) - 1);
-        bool any = false;
+template <int D, int CP>
+__global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+    pdl_wait();
+    using Ring = TileRing<D, false>;
+    constexpr int NE = Queries<D, CP>::NE;
+    extern __shared__ __align__(128) unsigned char rings[];
+    __shared__ uint64_t bars[AT_WARPS][Ring::NST];
+    __shared__ int4 infos[AT_WARPS][Ring::NST];
+    __shared__ Plan<AT_THREADS> plan;
+    plan.make(a);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+    const int w = blockIdx.x * AT_WARPS + warp;
+    if (w >= plan.warps(a)) return;
+    const int G = a.Hq / a.Hkv;
+    Ring ring;
+    ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
+    const size_t row_len = (size_t)a.max_pages * a.P;
+    long long t = plan.first_of(a, w);
+    const long long end = plan.first_of(a, w + 1);
+    Walk walk;
+    walk.to(a, plan, t);
+    while (t < end) {
+        const Share sh = walk.share(a, t, end);
+        t += sh.last - sh.first;
+        ring.start();
+        for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        const int h0 = sh.b * a.Hq + sh.kvh * G;
+        Queries<D, CP> Q;
+        Q.load(a.q + (size_t)h0 * D, G, (a.alpha - 1.f) * rsqrtf((float)D));
+        const size_t list = (size_t)h0 * row_len + (size_t)sh.first * 16;
+
+        float m[2] = {-INFINITY, -INFINITY};      // the share's max so far, of the lane's columns
+        float known[2] = {-INFINITY, -INFINITY};  // what other shares of the head have reported
+        int next[2] = {ORD_NEG_INF, ORD_NEG_INF};
+        int n[CP] = {};                           // candidates of each head
+        bool bad[2] = {false, false};             // the lane saw a NaN score
+        for (int i = sh.first; i < sh.last; ++i) {
+            int4 what;
+            unsigned char *tile;
+            if (!ring.take(a, what, tile)) {
+                ring.drain(a);
+                return;
+            }
+            if (a.zmax && (ring.taken & 3) == 1) {  // used four tiles on: nothing waits for the load
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            if (r + 8 * (v >> 1) >= ta.nval || !((mask >> (2 * c + (v & 1))) & 1)) z[v] = -INFINITY;
-            any |= !(z[v] <= m[v & 1] - 1.f);  // NaN stays a candidate
-        }
-        if (!__any_sync(FULL, any)) continue;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
-            float tm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
-            m[e] = fmaxf(m[e], tm);
-        }
-        const unsigned row = (unsigned)ta.blk * a.P + 16 * ta.t16 + r;
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            if (h >= G) break;
-            const int e = h & 1;
-            const bool mine = c == (h >> 1);
-            const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= m[e] - 1.f));
-            const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= m[e] - 1.f));
-            if (lo | hi) {
-                const size_t at = (h0 + h) * row_len + (size_t)sp.first * 16 + n[h];
-                const unsigned below = (1u << lane) - 1u;
-                if ((lo >> lane) & 1u) {
-                    const size_t k = at + __popc(lo & below);
-                    a.cand_z[k] = z[e];
-                    a.cand_row[k] = row;
+                for (int e = 0; e < NE; ++e) {
+                    known[e] = fmaxf(known[e], ord2f(next[e]));
+                    if (2 * c + e < G) next[e] = __ldcg(a.zmax + h0 + 2 * c + e);
                 }
-                if ((hi >> lane) & 1u) {
-                    const size_t k = at + __popc(lo) + __popc(hi & below);
-                    a.cand_z[k] = z[2 + e];
-                    a.cand_row[k] = row + 8;
+            }
+            float z[4];
+            bool any = false;
+            if (what.x >= 0) {
+                tile_scores<D, CP>(tile, Q, z);
+                mask_scores<CP>(what, G, z);
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float thr = fmaxf(m[e], known[e]) - 1.f;
+                    any |= !(z[e] <= thr) || !(z[2 + e] <= thr);  // NaN stays a candidate
                 }
-                n[h] += __popc(lo) + __popc(hi);
+            }
+            __syncwarp();
+            if (i + Ring::NST < sh.last) ring.issue(a, sh, i + Ring::NST);
+            if (!__any_sync(FULL, any)) continue;
+            float thr[2];
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
+                float tm = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
+                if (tm > m[e]) {
+                    m[e] = tm;
+                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < min(CP, G))
+                        atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
+                }
+                thr[e] = fmaxf(m[e], known[e]) - 1.f;
+            }
+            const unsigned row = (unsigned)what.x * a.P + 16 * what.w + r;
+#pragma unroll
+            for (int h = 0; h < CP; ++h) {
+                if (h >= G) break;
+                const int e = h & 1;
+                const bool mine = c == (h >> 1);
+                const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
+                const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
+                if (lo | hi) {
+                    const size_t at = list + h * row_len + n[h];
+                    const unsigned below = (1u << lane) - 1u;
+                    if ((lo >> lane) & 1u) {
+                        const size_t k = at + __popc(lo & below);
+                        a.cand_z[k] = z[e];
+                        a.cand_row[k] = row;
+                    }
+                    if ((hi >> lane) & 1u) {
+                        const size_t k = at + __popc(lo) + __popc(hi & below);
+                        a.cand_z[k] = z[2 + e];
+                        a.cand_row[k] = row + 8;
+                    }
+                    n[h] += __popc(lo) + __popc(hi);
+                }
             }
         }
-    }
+        const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        float mh = __shfl_sync(FULL, m[h & 1], h >> 1);
-        // a NaN stays a candidate: its segment may not be passed over for a low max
-        if (__any_sync(FULL, c == (h >> 1) && bad[h & 1])) mh = __int_as_float(0x7fc00000);
-        if (h < G && lane == 0) {
-            a.seg_n[(size_t)(h0 + h) * a.seg_len + seg] = n[h];
-            a.seg_max[(size_t)(h0 + h) * a.seg_len + seg] = mh;
+        for (int h = 0; h < CP; ++h) {
+            float mh = __shfl_sync(FULL, m[h & 1], h >> 1);
+            // a NaN stays a candidate: its share may not be passed over for a low max
+            if (__any_sync(FULL, c == (h >> 1) && bad[h & 1])) mh = __int_as_float(0x7fc00000);
+            if (h < G && lane == 0) a.seg[slot * G + h] = make_int2(n[h], __float_as_int(mh));
         }
     }
 }
@@ -466,37 +850,47 @@ constexpr int TK_NT = 256;
 constexpr int TK_NW = TK_NT / 32;
 constexpr int TK_CAP = 4096;  // candidates held on chip
 
-// One CTA a head: the candidates above the head's max - 1 in list order, their
+// One CTA a head: the candidates above the head's max - 1 in token order, their
 // threshold, and the sum of p v over the support.
 template <int D>
 __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int NG = Kv4<D>::NG;
-    extern __shared__ int seg_at[];  // [W + 1] place of each segment's candidates
-    __shared__ float cz[TK_CAP];
-    __shared__ unsigned crow[TK_CAP];
+    extern __shared__ int dyn[];
+    float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates ...
+    unsigned *crow = reinterpret_cast<unsigned *>(dyn + TK_CAP);    // [TK_CAP] ... and their value rows
+    float *raw_z = reinterpret_cast<float *>(dyn + 2 * TK_CAP);     // [TK_CAP] listed, before the cut
+    int *raw_at = dyn + 3 * TK_CAP;                                 // [TK_CAP]
+    int *seg_at = dyn + 4 * TK_CAP;                                 // [shares + 1] place of each share's candidates
+    __shared__ Plan<TK_NT> plan;
     __shared__ float o_sh[TK_NW][D];
     __shared__ float red[2][TK_NW][2];
     __shared__ float s_max[TK_NW];
+    __shared__ int s_n[TK_NW];
     __shared__ int scan[72];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.Hkv;
     int b, h;
     head_of(blockIdx.x, a.kv0 * G, a.nk * G, b, h);
     const int bh = b * a.Hq + h, kvh = h / G;
-    const int W = a.S * AT_WARPS;
     const float nan = __int_as_float(0x7fc00000);
     const uint16_t qb = threadIdx.x < D ? a.q[(size_t)bh * D + threadIdx.x] : (uint16_t)0;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.B; i += TK_NT)
+            if (a.seq_lens[i] > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
+    plan.make(a);
+    const GroupSlots gs = group_slots(a, plan, b, kvh);
+    const int W = gs.w1 - gs.w0 + 1;
+    const int2 *seg = a.seg + (a.kv0 * slots_per_head(a.B) + gs.w0 + gs.g) * G + h % G;
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
 
-    const int *sn = a.seg_n + (size_t)bh * a.seg_len;
-    const float *sm = a.seg_max + (size_t)bh * a.seg_len;
     float zmax = -INFINITY;
     int listed = 0;
     for (int i = threadIdx.x; i < W; i += TK_NT) {
-        zmax = fmaxf(zmax, __ldcg(sm + i));
-        listed |= __ldcg(sn + i);
+        const int2 s = __ldcg(seg + (size_t)i * G);
+        zmax = fmaxf(zmax, __int_as_float(s.y));
+        listed |= s.x;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) zmax = fmaxf(zmax, __shfl_xor_sync(FULL, zmax, o));
@@ -513,44 +907,39 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     }
 
     const float thr = zmax - 1.f;
-    const int seq = seq_len_of(a.seq_lens, b, a.P, a.max_pages, nullptr);
-    const long long T = (long long)(a.union_e ? a.union_cnt[b * a.Hkv + kvh] : n_pages_of(seq, a.P)) * (a.P / 16);
     const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
-    auto seg_base = [&](int w) { return (size_t)(T * w / W) * 16; };
-
-    // how many of each segment stay, and where they go
-    for (int w = warp; w < W; w += TK_NW) {
-        const int n = __ldcg(sn + w);
-        const float *src = zl + seg_base(w);
-        int k = 0;
-        if (!(__ldcg(sm + w) <= thr))
-            for (int i = lane; i < n; i += 32) k += !(__ldcg(src + i) <= thr);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) k += __shfl_xor_sync(FULL, k, o);
-        if (lane == 0) seg_at[w] = k;
-    }
-    __syncthreads();
-    int nc = 0;
-    for (int w0 = 0; w0 < W; w0 += TK_NT) {
-        const int w = w0 + threadIdx.x;
-        const int k = w < W ? seg_at[w] : 0;
-        int tot;
-        const int at = block_excl_scan(k, scan, &tot);
-        if (w < W) seg_at[w] = nc + at;
-        nc += tot;
-    }
-    if (threadIdx.x == 0) seg_at[W] = nc;
-    __syncthreads();
-    const bool onchip = nc <= TK_CAP;
-    bool bad = false;
-    // every kept candidate: f(place, z, row)
+    // first place of a share's list in the head's
+    auto seg_base = [&](int w) { return (int)max(0ll, plan.first_of(a, gs.w0 + w) - gs.start) * 16; };
+    // listed candidates of a share that reaches the cut
+    auto seg_size = [&](int w) {
+        const int2 s = __ldcg(seg + (size_t)w * G);
+        return __int_as_float(s.y) <= thr ? 0 : s.x;
+    };
+    // exclusive sums of f(w) over the shares, in seg_at; returns the total
+    auto place = [&](auto f) {
+        long long all = 0;
+        for (int w0 = 0; w0 < W; w0 += TK_NT) {
+            const int w = w0 + threadIdx.x;
+            const int k = w < W ? f(w) : 0;
+            int tot;
+            const int at = block_excl_scan(k, scan, &tot);
+            if (w < W) seg_at[w] = (int)all + at;
+            all += tot;
+        }
+        if (threadIdx.x == 0) seg_at[W] = (int)all;
+        __syncthreads();
+        return (int)all;
+    };
+    const int R = place(seg_size);
+    int nc;
+    bool onchip = true, bad = false;
+    // every kept candidate, a warp a share: f(place, z, index in the head's list)
     auto each = [&](auto f) {
         for (int w = warp; w < W; w += TK_NW) {
             int at = seg_at[w];
             if (at == seg_at[w + 1]) continue;
-            const int n = __ldcg(sn + w);
-            const size_t src = seg_base(w);
+            const int n = seg_size(w), src = seg_base(w);
             for (int i0 = 0; i0 < n; i0 += 32) {
                 const float z = i0 + lane < n ? __ldcg(zl + src + i0 + lane) : -INFINITY;
                 const bool keep = !(z <= thr);
@@ -560,13 +949,74 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             }
         }
     };
-    each([&](int at, float z, size_t i) {
-        bad |= z != z;
-        if (onchip) {
-            cz[at] = z;
-            crow[at] = __ldcg(rl + i);
+    if (R <= TK_CAP) {
+        // the lists as one range, a contiguous piece a warp
+        const int piece = ((R + TK_NT - 1) / TK_NT) * 32;
+        const int i1 = min(R, (warp + 1) * piece);
+        int kept = 0;
+        for (int i0 = warp * piece; i0 < i1; i0 += 32) {
+            const int i = i0 + lane;
+            bool keep = false;
+            if (i < i1) {
+                int lo = 0, hi = W - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (seg_at[mid] <= i) lo = mid;
+                    else hi = mid - 1;
+                }
+                const int at = seg_base(lo) + i - seg_at[lo];
+                const float z = __ldcg(zl + at);
+                raw_z[i] = z;
+                raw_at[i] = at;
+                keep = !(z <= thr);
+                bad |= z != z;
+            }
+            kept += __popc(__ballot_sync(FULL, keep));
         }
-    });
+        if (lane == 0) s_n[warp] = kept;
+        __syncthreads();
+        int at = 0;
+        nc = 0;
+#pragma unroll
+        for (int w = 0; w < TK_NW; ++w) {
+            if (w < warp) at += s_n[w];
+            nc += s_n[w];
+        }
+        for (int i0 = warp * piece; i0 < i1; i0 += 32) {
+            const int i = i0 + lane;
+            const float z = i < i1 ? raw_z[i] : -INFINITY;
+            const bool keep = !(z <= thr);
+            const unsigned bal = __ballot_sync(FULL, keep);
+            if (keep) {
+                const int k = at + __popc(bal & ((1u << lane) - 1u));
+                cz[k] = z;
+                crow[k] = __ldcg(rl + raw_at[i]);
+            }
+            at += __popc(bal);
+        }
+    } else {
+        // how many of each share stay, and where they go
+        for (int w = warp; w < W; w += TK_NW) {
+            const int n = seg_size(w);
+            const float *src = zl + seg_base(w);
+            int k = 0;
+            for (int i = lane; i < n; i += 32) k += !(__ldcg(src + i) <= thr);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) k += __shfl_xor_sync(FULL, k, o);
+            __syncwarp();
+            if (lane == 0) seg_at[w] = k;
+        }
+        __syncthreads();
+        nc = place([&](int w) { return seg_at[w]; });
+        onchip = nc <= TK_CAP;
+        each([&](int at, float z, int i) {
+            bad |= z != z;
+            if (onchip) {
+                cz[at] = z;
+                crow[at] = __ldcg(rl + i);
+            }
+        });
+    }
     if (__syncthreads_or(bad)) {
         for (int j = threadIdx.x; j < D; j += TK_NT) a.out[(size_t)bh * D + j] = nan;
         if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = nan;
@@ -581,7 +1031,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             tau = entmax_tau<TK_NT>([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); }, nc,
                                     thr, hi, zmax, r, ri, red);
         else  // every thread adds the candidates of its place, pass by pass
-            tau = entmax_tau<TK_NT>([&](auto add, int, int) { each([&](int, float z, size_t) { add(z); }); }, nc, thr, hi,
+            tau = entmax_tau<TK_NT>([&](auto add, int, int) { each([&](int, float z, int) { add(z); }); }, nc, thr, hi,
                                     zmax, r, ri, red);
     }
     if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = tau;
@@ -602,8 +1052,9 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         const unsigned char *tile = a.v4 + ((size_t)blk * a.Hkv + kvh) * rec + (size_t)(slot >> 4) * Kv4<D>::TILE;
         // the lane's coordinate block keeps its place: read the word that holds it
         const unsigned w =
-            rotr3(__ldg(reinterpret_cast<const unsigned *>(tile) + pair * (D / 4) +
-                        (piece ^ kv4_vswz<D>(pair)) * Kv4<D>::WPL + wi)) >>
+            rotr(__ldg(reinterpret_cast<const unsigned *>(tile) + pair * (D / 4) +
+                       (piece ^ kv4_vswz<D>(pair)) * Kv4<D>::WPL + wi),
+                 3) >>
             (16 * (t & 1));
         const unsigned pr = __ldg(reinterpret_cast<const unsigned *>(tile + Kv4<D>::CODES) + t * NG + (wi >> 1));
         const float s = p * bf16lo(pr), lo = p * bf16hi(pr);
@@ -611,12 +1062,13 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         for (int i = 0; i < 4; ++i) acc[i] += fmaf(s, (float)((w >> (4 * i)) & 15u), lo);
     };
     if (onchip) {
+#pragma unroll 4
         for (int i = warp * RPW + sub; i < nc; i += TK_NW * RPW) add_row(cz[i], crow[i]);
     } else {
         for (int w = warp; w < W; w += TK_NW) {
             if (seg_at[w] == seg_at[w + 1]) continue;
-            const int n = __ldcg(sn + w);
-            const size_t src = seg_base(w);
+            const int n = seg_size(w), src = seg_base(w);
+#pragma unroll 4
             for (int i = sub; i < n; i += RPW) {
                 const float z = __ldcg(zl + src + i);
                 if (z > tau) add_row(z, __ldcg(rl + src + i));
@@ -642,23 +1094,23 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 
 // --------------------------------------------------------------- launch
 
-// Splits a group's page list is cut into.
-int splits(const entmaxkv_shape *s, int nk) {
-    const long long tiles = (long long)s->max_pages * (s->page_size / 16);
+// Warps that share the tiles of a call over nk kv heads, on `ctas` CTAs an SM:
+// the grid fills the GPU once, unless that leaves fewer than AT_MIN_TILES
+// tiles to a warp or cuts each group's list in more than AT_GROUP_PARTS.
+int share_warps(const entmaxkv_shape *s, int nk, int sms, int ctas) {
     const long long groups = (long long)s->B * nk;
-    long long S = AT_SPLIT_CTAS / groups;
-    const long long most = (tiles + AT_WARPS * AT_MIN_TILES - 1) / (AT_WARPS * AT_MIN_TILES);
-    if (S > most) S = most;
-    return S < 1 ? 1 : (int)S;
+    const long long tiles = groups * s->max_pages * (s->page_size / 16);
+    long long W = (long long)sms * ctas * AT_WARPS;
+    if (W > AT_MAX_WARPS) W = AT_MAX_WARPS;
+    if (W > groups * AT_GROUP_PARTS) W = groups * AT_GROUP_PARTS;
+    if (W > (tiles + AT_MIN_TILES - 1) / AT_MIN_TILES) W = (tiles + AT_MIN_TILES - 1) / AT_MIN_TILES;
+    return (int)W;
 }
 
 struct Carve {
-    size_t part, cand_z, cand_row, seg_n, seg_max, union_e, union_blk, union_cnt, zmax, counters, total;
+    size_t part_o, part_ml, cand_z, cand_row, seg, union_e, union_blk, union_cnt, zmax, counters, total;
 };
 
-// The regions hold full-size rows of every head, and as many splits as a call
-// on one kv head alone may use, so calls on disjoint kv-head ranges can share
-// the workspace.
 Carve carve(const entmaxkv_shape *s) {
     Carve c;
     size_t off = 0;
@@ -669,12 +1121,12 @@ Carve carve(const entmaxkv_shape *s) {
     };
     const size_t heads = (size_t)s->B * s->Hq, groups = (size_t)s->B * s->Hkv;
     const size_t tokens = heads * s->max_pages * s->page_size;
-    const size_t S = splits(s, 1);
-    c.part = take(S * heads * (s->d + 2) * 4);
+    const size_t rows = s->Hq * slots_per_head(s->B);
+    c.part_o = take(rows * s->d * 4);
+    c.part_ml = take(rows * 8);
     c.cand_z = take(tokens * 4);
     c.cand_row = take(tokens * 4);
-    c.seg_n = take(heads * S * AT_WARPS * 4);
-    c.seg_max = take(heads * S * AT_WARPS * 4);
+    c.seg = take(rows * 8);
     c.union_e = take(groups * s->max_pages * 4);
     c.union_blk = take(groups * s->max_pages * 4);
     c.union_cnt = take(groups * 4);
@@ -684,21 +1136,37 @@ Carve carve(const entmaxkv_shape *s) {
     return c;
 }
 
-template <int D>
+template <class K>
+cudaError_t run_shares(K k, const Kv4DecodeArgs &a, cudaStream_t st) {
+    const size_t smem = (size_t)AT_WARPS * AT_RING;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k), smem);
+    return e != cudaSuccess ? e : launch_pdl(k, dim3(ceil_div(a.W, AT_WARPS)), dim3(AT_THREADS), smem, st, a);
+}
+
+template <int D, int CP>
 cudaError_t decode_t(const Kv4DecodeArgs &a, cudaStream_t st) {
-    const int groups = a.B * a.nk, heads = groups * (a.Hq / a.Hkv);
+    const int heads = a.B * a.nk * (a.Hq / a.Hkv);
     cudaError_t e;
     if (a.alpha == 1.f) {
-        e = launch_pdl(kv4_softmax_kernel<D>, dim3(groups * a.S), dim3(AT_THREADS), 0, st, a);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(D), 0, st, a);
+        if ((e = run_shares(kv4_softmax_kernel<D, CP>, a, st)) != cudaSuccess) return e;
+        return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(CB_NT), (size_t)a.W * 4, st, a);
     }
-    e = launch_pdl(kv4_scan_kernel<D>, dim3(groups * a.S), dim3(AT_THREADS), 0, st, a);
-    if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)(a.S * AT_WARPS + 1) * 4;
+    if (a.zmax && !a.union_e) {
+        e = launch_pdl(kv4_reset_kernel, dim3(ceil_div(heads, 256)), dim3(256), 0, st, a);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = run_shares(kv4_scan_kernel<D, CP>, a, st)) != cudaSuccess) return e;
+    const size_t smem = (size_t)(4 * TK_CAP + a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
     return launch_pdl(k, dim3(heads), dim3(TK_NT), smem, st, a);
+}
+
+template <int D>
+cudaError_t decode_d(const Kv4DecodeArgs &a, cudaStream_t st) {
+    const int G = a.Hq / a.Hkv;
+    return G == 1 ? decode_t<D, 1>(a, st) : G == 2 ? decode_t<D, 2>(a, st) : G <= 4 ? decode_t<D, 4>(a, st)
+                                                                                    : decode_t<D, 8>(a, st);
 }
 
 }  // namespace
@@ -738,11 +1206,12 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.seq_lens = seq_lens;
     a.out = out;
     a.tau_out = tau_out;
-    a.part = reinterpret_cast<float *>(w + c.part);
+    a.part_o = reinterpret_cast<float *>(w + c.part_o);
+    a.part_ml = reinterpret_cast<float2 *>(w + c.part_ml);
     a.cand_z = reinterpret_cast<float *>(w + c.cand_z);
     a.cand_row = reinterpret_cast<unsigned *>(w + c.cand_row);
-    a.seg_n = reinterpret_cast<int *>(w + c.seg_n);
-    a.seg_max = reinterpret_cast<float *>(w + c.seg_max);
+    a.seg = reinterpret_cast<int2 *>(w + c.seg);
+    a.zmax = reinterpret_cast<int *>(w + c.zmax);
     a.B = s->B;
     a.Hq = s->Hq;
     a.Hkv = s->Hkv;
@@ -750,8 +1219,10 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.max_pages = s->max_pages;
     a.num_blocks = s->num_blocks;
     kv_range(s, &a.kv0, &a.nk);
-    a.S = splits(s, a.nk);
-    a.seg_len = splits(s, 1) * AT_WARPS;
+    a.lp = s->page_size == 16 ? 0 : s->page_size == 32 ? 1 : 2;
+    a.W = share_warps(s, a.nk, di.sms, alpha == 1.f ? 3 : 5);
+    // short shares list little that a common max would have cut: no launch to reset it
+    if (!sel && (long long)s->B * a.nk * s->max_pages << a.lp < 8ll * a.W) a.zmax = nullptr;
     a.alpha = alpha;
     a.r_int = alpha > 1.f ? integer_r(alpha) : 0;
     a.status = di.status;
@@ -783,7 +1254,7 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
         a.union_blk = u.ws.union_blk;
         a.union_cnt = u.ws.union_cnt;
     }
-    const cudaError_t e = s->d == 64 ? decode_t<64>(a, st) : decode_t<128>(a, st);
+    const cudaError_t e = s->d == 64 ? decode_d<64>(a, st) : decode_d<128>(a, st);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA;
 }
 

@@ -143,9 +143,10 @@ __device__ __forceinline__ unsigned join_k(const unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     unsigned w;
     if constexpr (D == 128) {
-        w = (c[0] | (c[1] << 16) | (c[2] << 4) | (c[3] << 20)) << (8 * (lane & 1));
+        const int p = 8 * (lane & 1);
+        w = rotl(kv4_key_pair(c[0], c[1]), p) | rotl(kv4_key_pair(c[2], c[3]), p + 4);
     } else {
-        w = (c[0] | (c[1] << 16)) << (4 * (lane & 3));
+        w = rotl(kv4_key_pair(c[0], c[1]), 4 * (lane & 3));
         w |= __shfl_xor_sync(FULL, w, 2);
     }
     return w | __shfl_xor_sync(FULL, w, 1);
@@ -165,22 +166,22 @@ template <int D>
 __device__ __forceinline__ void split_k(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     if constexpr (D == 128) {
-        const unsigned w = rotr3(tile[kv4_kword<D>(t, lane >> 1)]) >> (8 * (lane & 1));
-        c[0] = w & 15;
-        c[1] = (w >> 16) & 15;
-        c[2] = (w >> 4) & 15;
-        c[3] = (w >> 20) & 15;
+        const unsigned w = rotr(tile[kv4_kword<D>(t, lane >> 1)], 8 * (lane & 1)), x = rotr(w, 4);
+        c[0] = kv4_key_code(w);
+        c[1] = kv4_key_code(w >> 16);
+        c[2] = kv4_key_code(x);
+        c[3] = kv4_key_code(x >> 16);
     } else {
-        const unsigned w = rotr3(tile[kv4_kword<D>(t, lane >> 2)]) >> (4 * (lane & 3));
-        c[0] = w & 15;
-        c[1] = (w >> 16) & 15;
+        const unsigned w = rotr(tile[kv4_kword<D>(t, lane >> 2)], 4 * (lane & 3));
+        c[0] = kv4_key_code(w);
+        c[1] = kv4_key_code(w >> 16);
     }
 }
 template <int D>
 __device__ __forceinline__ void split_v(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     const int q4 = D == 128 ? lane : lane >> 1;
-    unsigned w = rotr3(tile[kv4_vword<D>(t >> 1, q4)]) >> (16 * (t & 1));
+    unsigned w = rotr(tile[kv4_vword<D>(t >> 1, q4)], 3) >> (16 * (t & 1));
     if constexpr (D == 64) w >>= 8 * (lane & 1);
 #pragma unroll
     for (int i = 0; i < CPL<D>; ++i) c[i] = (w >> (4 * i)) & 15;
@@ -206,7 +207,7 @@ __device__ __forceinline__ void write_key(unsigned char *tile, int t, const floa
     unsigned c[CPL<D>];
     float s, lo;
     quantise<D>(x, c, s, lo);
-    const unsigned w = rotl3(join_k<D>(c));
+    const unsigned w = join_k<D>(c);
     const int lane = threadIdx.x & 31;
     constexpr int SH = D == 128 ? 2 : 4;  // lanes of a word
     if (lane % SH == 0) reinterpret_cast<unsigned *>(tile)[kv4_kword<D>(t, lane / SH)] = w;
@@ -284,10 +285,10 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_cons
             unsigned *w = reinterpret_cast<unsigned *>(vtile) + kv4_vword<D>((t & 15) >> 1, lane / SH);
             unsigned v = half[0] | (half[1] << 16);
             if (!(has0 && has1)) {  // the other token of the pair keeps its half
-                const unsigned old = rotr3(*w);
+                const unsigned old = rotr(*w, 3);
                 v = has0 ? (half[0] | (old & 0xffff0000u)) : ((half[1] << 16) | (old & 0xffffu));
             }
-            *w = rotl3(v);
+            *w = rotl(v, 3);
         }
     }
     if (!meta) return;
