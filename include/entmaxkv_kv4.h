@@ -23,15 +23,11 @@
  * Layout: cache[block][kv head][P / 16 tiles][9 d bytes].  A tile holds 16
  * consecutive tokens: 8 d bytes of codes, then for each token and each group
  * of 64 coordinates a 32-bit word, s in the low and lo in the high half.
- * Codes lie in 32-bit words w, so that the attention kernel makes bf16 numbers
- * of two codes by a rotation and a mask:
+ * Codes lie in 32-bit words:
  *   keys    token t, coordinate j = 64 g + 16 c + 8 i + n: word
- *           t d/8 + c d/32 + 2 g + i.  Code x is sign and magnitude of
- *           2 x - 15 = +-(2 m + 1): the sign (1: negative) at bit 15 + k, m at
- *           bits 4 + k to 6 + k, counted modulo 32, k = 16 (n & 1) + 4 (n >> 1)
+ *           t d/8 + c d/32 + 2 g + i, bits 16 (n & 1) + 4 (n >> 1)
  *   values  token t, coordinate j = 64 g + 8 r + 4 i + n: word
- *           (t >> 1) d/4 + (r ^ x) d/32 + 2 g + i, bits 16 (t & 1) + 4 n, the
- *           word then rotated left by 3,
+ *           (t >> 1) d/4 + (r ^ x) d/32 + 2 g + i, bits 16 (t & 1) + 4 n,
  *           x = 2 ((t >> 1) & 3) for d = 128, 4 ((t >> 2) & 1) for d = 64
  *           (keeps the eight-token reads of the attention kernel on distinct
  *           shared-memory banks)

@@ -25,7 +25,7 @@ __device__ __forceinline__ size_t kv4_tile(int blk, int Hkv, int kvh, int P, int
 }
 
 // Word index (within the tile) of the 8 coordinates 8 q8 .. 8 q8 + 7 of the
-// key of token t; coordinate n of them in half n & 1 of pair n >> 1.
+// key of token t; coordinate n of them at bits 16 (n & 1) + 4 (n >> 1).
 template <int D>
 __device__ __forceinline__ int kv4_kword(int t, int q8) {
     return t * (D / 8) + ((q8 >> 1) & 3) * Kv4<D>::WPL + 2 * (q8 >> 3) + (q8 & 1);
@@ -40,19 +40,6 @@ __device__ __forceinline__ int kv4_vswz(int pair) {
 template <int D>
 __device__ __forceinline__ int kv4_vword(int pair, int q4) {
     return pair * (D / 4) + (((q4 >> 1) & 7) ^ kv4_vswz<D>(pair)) * Kv4<D>::WPL + 2 * (q4 >> 4) + (q4 & 1);
-}
-__device__ __forceinline__ unsigned rotl(unsigned w, int n) { return __funnelshift_l(w, w, n); }
-__device__ __forceinline__ unsigned rotr(unsigned w, int n) { return __funnelshift_r(w, w, n); }
-// Key code c as 16 bits: 2 c - 15 = +-(2 m + 1), the sign in bit 15 and m in
-// bits 4 to 6.  A word holds four pairs of these, pair p rotated left by 4 p
-// (the bits of the eight codes tile the word).
-__device__ __forceinline__ unsigned kv4_key_bits(unsigned c) { return c & 8 ? (c & 7) << 4 : 0x8000u | ((7 - c) << 4); }
-__device__ __forceinline__ unsigned kv4_key_pair(unsigned c0, unsigned c1) {
-    return kv4_key_bits(c0) | (kv4_key_bits(c1) << 16);
-}
-__device__ __forceinline__ unsigned kv4_key_code(unsigned x) {
-    const unsigned m = (x >> 4) & 7;
-    return x & 0x8000u ? 7 - m : 8 + m;
 }
 
 struct Kv4RowArgs {

@@ -3,22 +3,26 @@
 //
 // Mathematics.  With k_tj = s_tg c_tj + lo_tg for the coordinates j of group
 // g, the score of token t is
-//   q.k_t = sum_g [ s_tg sum_{j in g} q_j (c_tj - 7.5) + (lo_tg + 7.5 s_tg) sum_{j in g} q_j ],
-// so the centred codes themselves are the tensor-core operand.  They are
-// centred because the tensor core truncates its fp32 sums: an offset common
-// to all codes would be summed, truncated and cancelled again (with 16 + c
-// as the operand the softmax of 32k tokens was 5e-4 off, relatively).
-//   keys    2 c - 15 is +-(2 m + 1), m < 8: sign and m are stored so that one
-//           rotation and one mask leave the bf16 subnormal +-(2 m + 1) 2^-130;
-//           the query is scaled by a power of two per head, which is exact
-//           and keeps the products normal
-//   values  a code in the top mantissa bits of a bf16 with exponent 4 is 16 +
-//           c; a packed subtraction makes it c - 7.5, exactly.  The weights
-//           p_t s_tg go in as three bf16 parts (24 bits together) and sum_t
-//           p_t (lo_tg + 7.5 s_tg) is added at the end.  Groups of four heads
-//           or fewer put the parts in the columns their heads leave free.
-//           The sums move to a second set of fp32 registers every four tiles,
-//           so that few truncations meet a large sum.
+//   q.k_t = sum_g [ s_tg sum_{j in g} q_j (c_tj - 8) + (lo_tg + 8 s_tg) sum_{j in g} q_j ],
+// so the centred codes themselves are the tensor-core operand, in fp16: a code
+// in the mantissa of 1024 is 1024 + c or 1024 + 16 c, and one packed
+// multiply-add makes that c - 8, exactly (fp16 has room for two codes in a
+// mantissa, so a word of eight codes needs one shift; bf16 would need three,
+// and integer shifts and masks are what such a kernel is bound by).  The
+// codes are centred because the tensor core truncates its fp32 sums: an offset
+// common to all codes would be summed, truncated and cancelled again (with 16
+// + c as the operand the softmax of 32k tokens was 5e-4 off, relatively).
+//   keys    the query is scaled by a power of two per head, so that its
+//           largest coordinate is near 2^13: coordinates down to 2^-27 of
+//           that stay exact, smaller ones are off by 2^-38 of it at most
+//   values  the weights p_t s_tg go in as two fp16 parts (22 bits together),
+//           and sum_t p_t (lo_tg + 8 s_tg) is added at the end.  The
+//           reference of a head's softmax is placed so that its largest p s
+//           lies between 2^9 and 2^15: what is lost of a weight is below 2^-34
+//           of the largest.  Groups of four heads or fewer put the two parts
+//           in the columns their heads leave free.  The sums move to a second
+//           set of fp32 registers every few tiles, so that few truncations
+//           meet a large sum.
 //
 // The tiles (16 tokens of one kv head) of all groups' page lists form one
 // range that is cut evenly among the warps of a grid that fills the GPU once:
@@ -51,8 +55,8 @@ constexpr int AT_RING = 9216;           // bytes of a warp's ring
 constexpr int AT_MAX_WARPS = 148 * 5 * AT_WARPS;
 constexpr int AT_MIN_TILES = 2;         // tiles a warp gets at least ...
 constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
-constexpr int AT_FLUSH = 4;             // tiles between flushes of the output sums
-constexpr float AT_SLACK = 6.f;         // how far (in powers of two) a score may exceed the reference max
+constexpr float AT_MAX_X = 32768.f;     // p s stays below this (fp16 ends at 65504) ...
+constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a reference is set
 
 struct Kv4DecodeArgs {
     const uint16_t *q;
@@ -278,30 +282,54 @@ struct TileRing {
 
 // --------------------------------------------------------------- operands
 
-// (2 c - 15) 2^-130 of pair p of a key word, as two bf16.
+// c - 8 of pair p of a word of eight codes (bits 4 p .. of each half), as two fp16.
 template <int p>
-__device__ __forceinline__ unsigned key_bf16(unsigned w) {
-    return ((p ? __funnelshift_r(w, w, 4 * p) : w) & 0x80708070u) | 0x00080008u;
-}
-// c - 7.5 of pair p of a value word, as two bf16: 16 + c less 23.5.
-template <int p>
-__device__ __forceinline__ unsigned value_bf16(unsigned w) {
-    const unsigned x = (((p == 0 ? w : p == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * p)) & 0x00780078u) | 0x41804180u);
+__device__ __forceinline__ unsigned code_f16(unsigned w) {
+    const unsigned x = p < 2 ? w : w >> 8;
     unsigned y;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3f803f80u), "r"(0xc1bcc1bcu));
+    if constexpr (p % 2 == 0)  // 1024 + c, less 1032
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"((x & 0x000f000fu) | 0x64006400u), "r"(0xe408e408u));
+    else  // 1024 + 16 c, over 16 and less 72
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(y)
+            : "r"((x & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
     return y;
+}
+// Two floats as fp16, x0 in the low half.
+__device__ __forceinline__ unsigned pack_f16(float x0, float x1) {
+    unsigned y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(x1), "f"(x0));
+    return y;
+}
+// What two floats exceed their fp16 parts by, as fp16 again.
+__device__ __forceinline__ unsigned rest_f16(float x0, float x1, unsigned hi) {
+    float h0, h1;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(h0), "=f"(h1)
+        : "r"(hi));
+    return pack_f16(x0 - h0, x1 - h1);
+}
+// The 8 x 8 matrix of 16-bit elements that the warp holds a row of in every
+// four lanes, transposed.
+__device__ __forceinline__ unsigned transpose8(unsigned x) {
+    unsigned y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// D = A(16x16 fp16, row) * B(16x8 fp16, col) + D, fp32 sums.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3,
+                                              unsigned b0, unsigned b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// The top halves of x0 and x1.
-__device__ __forceinline__ unsigned top_halves(float x0, float x1) {
-    return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
-}
-__device__ __forceinline__ float below_top(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-
 template <int N>
 __device__ __forceinline__ void load_words(const unsigned char *src, unsigned (&w)[N]) {
     if constexpr (N == 4) {
@@ -317,19 +345,19 @@ __device__ __forceinline__ void load_words(const unsigned char *src, unsigned (&
     }
 }
 
-// The group's queries as B fragments: column n holds head n % CP, scaled by
-// a power of two 2^e of its own; for the lane's two accumulator columns the
+// The G queries of a group as B fragments: column n holds head n % G, scaled
+// by a power of two 2^e of its own; for the lane's two accumulator columns the
 // sums of each coordinate group, in the units of the products, and the factor
 // from those units to z.
-template <int D, int CP>
+template <int D, int G>
 struct Queries {
-    static constexpr int NE = CP == 1 ? 1 : 2;  // distinct columns of a lane
+    static constexpr int NE = G == 1 ? 1 : 2;  // distinct columns of a lane
     unsigned b[D / 16][2];
     float sum[Kv4<D>::NG][NE];
     float factor[NE];
-    __device__ __forceinline__ void load(const uint16_t *q, int G, float scale) {
-        const int lane = threadIdx.x & 31, h = (lane >> 2) % CP, c = lane & 3;
-        const unsigned *qw = reinterpret_cast<const unsigned *>(q + (size_t)h * D);
+    __device__ __forceinline__ void load(const uint16_t *q, float scale) {
+        const int lane = threadIdx.x & 31, c = lane & 3;
+        const unsigned *qw = reinterpret_cast<const unsigned *>(q + (size_t)((lane >> 2) % G) * D);
         float t[Kv4<D>::NG];
         unsigned top = 0;
 #pragma unroll
@@ -343,7 +371,7 @@ struct Queries {
                     unsigned *d = b[2 * (2 * g + i) + k];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        d[x] = h < G ? qw[j0 / 2 + x] : 0u;
+                        d[x] = qw[j0 / 2 + x];
                         t[g] += bf16lo(d[x]) + bf16hi(d[x]);
                         top = max(top, max((d[x] >> 7) & 0xffu, (d[x] >> 23) & 0xffu));  // exponent fields
                     }
@@ -353,43 +381,55 @@ struct Queries {
         }
         top = max(top, __shfl_xor_sync(FULL, top, 1));
         top = max(top, __shfl_xor_sync(FULL, top, 2));
-        // the largest |q| goes to about 2^120: products with the subnormal
-        // codes stay normal down to 2^-110 of it, scaled sums below 2^127, and
-        // the factor below stays a normal number
-        const int E = max((int)top - 127, 0);
-        const int e = max(0, min(max(120 - E, 9), 127 - E));
+        const int e = min(13 - ((int)top - 127), 120);
         const float up = __uint_as_float((unsigned)(e + 127) << 23);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) b[i][x] = top_halves(bf16lo(b[i][x]) * up, bf16hi(b[i][x]) * up);
+            for (int x = 0; x < 2; ++x) b[i][x] = pack_f16(bf16lo(b[i][x]) * up, bf16hi(b[i][x]) * up);
 #pragma unroll
         for (int v = 0; v < NE; ++v) {
             const int src = 4 * (2 * c + v);
-            const int ec = __shfl_sync(FULL, e, src);
-            factor[v] = ldexpf(scale, 129 - ec);
+            const float upc = __shfl_sync(FULL, up, src);
+            factor[v] = scale / upc;
 #pragma unroll
-            for (int g = 0; g < Kv4<D>::NG; ++g) sum[g][v] = ldexpf(__shfl_sync(FULL, t[g], src), ec - 129);
+            for (int g = 0; g < Kv4<D>::NG; ++g) sum[g][v] = __shfl_sync(FULL, t[g], src) * upc;
+        }
+    }
+};
+
+// s and lo + 8 s of tokens lane / 4 and lane / 4 + 8.
+template <int D>
+struct Params {
+    float s[2][Kv4<D>::NG], o[2][Kv4<D>::NG];
+    __device__ __forceinline__ void load(const unsigned char *tile) {
+        constexpr int NG = Kv4<D>::NG;
+        const unsigned *pp = reinterpret_cast<const unsigned *>(tile + Kv4<D>::CODES) + ((threadIdx.x & 31) >> 2) * NG;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            unsigned w[NG];
+            if constexpr (NG == 2) load_words<2>(reinterpret_cast<const unsigned char *>(pp + 8 * u * NG), w);
+            else w[0] = pp[8 * u];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                s[u][g] = bf16lo(w[g]);
+                o[u][g] = fmaf(8.f, s[u][g], bf16hi(w[g]));
+            }
         }
     }
 };
 
 // z of the 16 tokens of a tile: z[e] token lane / 4, z[2 + e] token lane / 4 +
 // 8, columns 2 (lane % 4) + e.
-template <int D, int CP>
-__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D, CP> &Q, float (&z)[4]) {
-    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, NE = Queries<D, CP>::NE;
+template <int D, int G>
+__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D, G> &Q, float (&z)[4]) {
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, NE = Queries<D, G>::NE;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     unsigned w0[WPL], w1[WPL];
     load_words<WPL>(tile + r * (D / 2) + c * (4 * WPL), w0);
     load_words<WPL>(tile + (r + 8) * (D / 2) + c * (4 * WPL), w1);
-    const unsigned *pp = reinterpret_cast<const unsigned *>(tile + Kv4<D>::CODES);
-    unsigned p0[NG], p1[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        p0[g] = pp[r * NG + g];
-        p1[g] = pp[(r + 8) * NG + g];
-    }
+    Params<D> P;
+    P.load(tile);
 #pragma unroll
     for (int v = 0; v < 4; ++v) z[v] = 0.f;
 #pragma unroll
@@ -397,43 +437,42 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 2 * g; i < 2 * g + 2; ++i) {
-            mma_bf16_16816(acc, key_bf16<0>(w0[i]), key_bf16<0>(w1[i]), key_bf16<1>(w0[i]), key_bf16<1>(w1[i]),
-                           Q.b[2 * i][0], Q.b[2 * i][1]);
-            mma_bf16_16816(acc, key_bf16<2>(w0[i]), key_bf16<2>(w1[i]), key_bf16<3>(w0[i]), key_bf16<3>(w1[i]),
-                           Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
+            mma_f16_16816(acc, code_f16<0>(w0[i]), code_f16<0>(w1[i]), code_f16<1>(w0[i]), code_f16<1>(w1[i]),
+                          Q.b[2 * i][0], Q.b[2 * i][1]);
+            mma_f16_16816(acc, code_f16<2>(w0[i]), code_f16<2>(w1[i]), code_f16<3>(w0[i]), code_f16<3>(w1[i]),
+                          Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
         }
-        const float s0 = bf16lo(p0[g]), s1 = bf16lo(p1[g]);
-        const float o0 = fmaf(7.5f, s0, bf16hi(p0[g])), o1 = fmaf(7.5f, s1, bf16hi(p1[g]));
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            z[e] = fmaf(s0, acc[e], fmaf(o0, Q.sum[g][e], z[e]));
-            z[2 + e] = fmaf(s1, acc[2 + e], fmaf(o1, Q.sum[g][e], z[2 + e]));
-        }
+        for (int v = 0; v < 4; ++v)
+            if ((v & 1) < NE) z[v] = fmaf(P.s[v >> 1][g], acc[v], fmaf(P.o[v >> 1][g], Q.sum[g][v & 1 & (NE - 1)], z[v]));
     }
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-        z[e] *= Q.factor[e];
-        z[2 + e] *= Q.factor[e];
-    }
-}
-// Tokens behind the sequence and heads that did not select the page: -inf.
-template <int CP>
-__device__ __forceinline__ void mask_scores(const int4 &what, int G, float (&z)[4]) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int heads = (1 << G) - 1;
-    const int mask = what.z & heads;
-    if (what.y >= 16 && mask == (1 << CP) - 1) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-        if (r + 8 * (v >> 1) >= what.y || !((mask >> ((2 * c + (v & 1)) % CP)) & 1)) z[v] = -INFINITY;
+        if ((v & 1) < NE) z[v] *= Q.factor[v & 1 & (NE - 1)];
+}
+// Whether head n % G of the group selected the page of the tile.
+template <int G>
+__device__ __forceinline__ bool keeps(const int4 &what, int n) { return (what.z >> (n % G)) & 1; }
+template <int G>
+__device__ __forceinline__ bool whole(const int4 &what) { return what.y >= 16 && (~what.z & ((1 << G) - 1)) == 0; }
+// Tokens behind the sequence and heads that did not select the page: -inf.
+template <int G>
+__device__ __forceinline__ void mask_scores(const int4 &what, float (&z)[4]) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    if (whole<G>(what)) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (r + 8 * (v >> 1) >= what.y || !keeps<G>(what, 2 * c + (v & 1))) z[v] = -INFINITY;
 }
 
 // -------------------------------------------------------------- softmax
 
-template <int D, int CP>
+template <int D, int G>
 __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
-    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, CP>::NE;
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, G>::NE;
+    constexpr int NB = G == 8 ? 2 : 1;  // products per value operand: both parts, or both in one
+    constexpr int FLUSH = 8 / NB;       // tiles between flushes of the output sums
     using Ring = TileRing<D, true>;
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][Ring::NST];
@@ -443,8 +482,7 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
     if (w >= plan.warps(a)) return;
-    const int G = a.Hq / a.Hkv;
-    const int part = r / CP;  // the part of the weights that column r carries
+    const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
     ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
     long long t = plan.first_of(a, w);
@@ -456,18 +494,18 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
         t += sh.last - sh.first;
         ring.start();
         for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
-        Queries<D, CP> Q;
+        Queries<D, G> Q;
         // z in powers of two
-        Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, G, 1.4426950408889634f * rsqrtf((float)D));
+        Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, 1.4426950408889634f * rsqrtf((float)D));
 
         float acc[MT][4], tot[MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][v] = tot[i][v] = 0.f;
-        float off[NG] = {};                 // head of column r: sum p (lo + 7.5 s), this lane's tokens
-        float m[2] = {-INFINITY, -INFINITY};  // reference max of the lane's columns
-        float l[2] = {0.f, 0.f};
+        // per column of the lane: the reference (weights are 2^(z - ref)), the
+        // sums of p and of p (lo + 8 s) over the lane's tokens
+        float ref[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, off[NG][2] = {};
         for (int i = sh.first; i < sh.last; ++i) {
             int4 what;
             unsigned char *tile;
@@ -476,24 +514,57 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                 return;
             }
             if (what.x >= 0) {
-                float z[4];
-                tile_scores<D, CP>(tile, Q, z);
-                mask_scores<CP>(what, G, z);
-                // the reference max follows only when a score passes it by AT_SLACK
-                bool up = false;
+                float z[4], p[4], x[NG][4];
+                tile_scores<D, G>(tile, Q, z);
+                mask_scores<G>(what, z);
+                const unsigned char *vt = tile + Kv4<D>::TILE;
+                Params<D> P;
+                P.load(vt);
+                const bool all = whole<G>(what);
+                if (!all) {  // rows behind the sequence may hold anything
 #pragma unroll
-                for (int e = 0; e < NE; ++e) up |= !(fmaxf(z[e], z[2 + e]) <= m[e] + AT_SLACK);
-                if (__any_sync(FULL, up)) {
+                    for (int u = 0; u < 2; ++u)
+                        if (r + 8 * u >= what.y)
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) P.s[u][g] = P.o[u][g] = 0.f;
+                }
+                auto weights = [&] {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if ((v & 1) >= NE) continue;
+                        p[v] = ex2(z[v] - ref[v & 1]);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            x[g][v] = p[v] * P.s[v >> 1][g];
+                            // so may pages of other heads
+                            if (!all && !keeps<G>(what, 2 * c + (v & 1))) x[g][v] = 0.f;
+                            sum += x[g][v];
+                        }
+                    }
+                    return sum;
+                };
+                if (__any_sync(FULL, !(weights() <= AT_MAX_X))) {
+                    // the reference follows the largest p s
                     float corr[2] = {1.f, 1.f};
 #pragma unroll
                     for (int e = 0; e < NE; ++e) {
-                        float tm = fmaxf(z[e], z[2 + e]);
+                        float zm = fmaxf(z[e], z[2 + e]);
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
-                        const float mn = fmaxf(m[e], tm);
-                        corr[e] = mn == -INFINITY ? 1.f : exp2f(m[e] - mn);
-                        m[e] = mn;
+                        for (int o = 4; o < 32; o <<= 1) zm = fmaxf(zm, __shfl_xor_sync(FULL, zm, o));
+                        float xm = 0.f;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            xm = fmaxf(xm, fmaxf(exp2f(z[e] - zm) * P.s[0][g], exp2f(z[2 + e] - zm) * P.s[1][g]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(FULL, xm, o));
+                        const int up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);  // xm < 2^(exponent + 1)
+                        const float nr = fmaxf(ref[e], zm - (float)max(-100, min(up, 60)));
+                        corr[e] = exp2f(ref[e] - nr);
+                        ref[e] = nr;
                         l[e] *= corr[e];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) off[g][e] *= corr[e];
                     }
                     if (NE == 1) corr[1] = corr[0];
 #pragma unroll
@@ -503,100 +574,53 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                             acc[k][v] *= corr[v & 1];
                             tot[k][v] *= corr[v & 1];
                         }
-                    const float c0 = __shfl_sync(FULL, corr[0], r >> 1), c1 = __shfl_sync(FULL, corr[1], r >> 1);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) off[g] *= (r & 1) ? c1 : c0;
+                    weights();
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float base = m[e] == -INFINITY ? 0.f : m[e];
-                    z[e] = ex2(z[e] - base);
-                    z[2 + e] = ex2(z[2 + e] - base);
-                    l[e] += z[e] + z[2 + e];
-                }
-                // weights of column r, tokens 2c, 2c + 1, 2c + 8, 2c + 9
-                float p[4];
+                    l[e] += p[e] + p[2 + e];
+                    const bool kept = all || keeps<G>(what, 2 * c + e);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int src = 4 * (2 * c + u) + (r >> 1);
-                    const float x0 = __shfl_sync(FULL, z[0], src), y0 = __shfl_sync(FULL, z[2], src);
-                    if constexpr (NE == 1) {
-                        p[u] = x0;
-                        p[2 + u] = y0;
-                    } else {
-                        const float x1 = __shfl_sync(FULL, z[1], src), y1 = __shfl_sync(FULL, z[3], src);
-                        p[u] = (r & 1) ? x1 : x0;
-                        p[2 + u] = (r & 1) ? y1 : y0;
+                    for (int g = 0; g < NG; ++g) {
+                        const float y = fmaf(p[e], P.o[0][g], fmaf(p[2 + e], P.o[1][g], off[g][e]));
+                        if (kept) off[g][e] = y;
                     }
                 }
-                const unsigned char *vt = tile + Kv4<D>::TILE;
                 unsigned w0[WPL], w1[WPL];
                 const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
                 load_words<WPL>(vt + c * D + piece, w0);
                 load_words<WPL>(vt + (c + 4) * D + piece, w1);
-                unsigned pr[4][NG];
-                const unsigned *vp = reinterpret_cast<const unsigned *>(vt + Kv4<D>::CODES);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    unsigned two[2 * NG];
-                    load_words<2 * NG>(reinterpret_cast<const unsigned char *>(vp + (2 * c + 8 * u) * NG), two);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        pr[2 * u][g] = two[g];
-                        pr[2 * u + 1][g] = two[NG + g];
-                    }
-                }
-                // rows behind the sequence, and rows of pages that the head
-                // did not select, count as zero whatever they hold
-                if (what.y < 16 || !((what.z >> (r % CP)) & 1)) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (2 * c + (u & 1) + 8 * (u >> 1) >= what.y || !((what.z >> (r % CP)) & 1))
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) pr[u][g] = 0u;
-                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float x[4], y[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float s = bf16lo(pr[u][g]);
-                        off[g] = fmaf(p[u], fmaf(7.5f, s, bf16hi(pr[u][g])), off[g]);
-                        x[u] = p[u] * s;
-                        y[u] = below_top(x[u]);
-                    }
-                    // the B fragments: columns of parts 0 and 1 (and 2), then the rest
-                    constexpr int NB = CP == 8 ? 3 : CP == 4 ? 2 : 1;
+                    // token by column, to column by token
                     unsigned bf[NB][2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const unsigned hi = top_halves(x[2 * u], x[2 * u + 1]);
-                        const unsigned mid = top_halves(y[2 * u], y[2 * u + 1]);
-                        const unsigned low = top_halves(below_top(y[2 * u]), below_top(y[2 * u + 1]));
-                        if constexpr (CP == 8) {
-                            bf[0][u] = hi;
-                            bf[NB / 2][u] = mid;
-                            bf[NB - 1][u] = low;
-                        } else if constexpr (CP == 4) {
-                            bf[0][u] = part ? mid : hi;
-                            bf[NB - 1][u] = part ? 0u : low;
+                        const float x0 = x[g][2 * u], x1 = x[g][2 * u + NE - 1];
+                        const unsigned hi = pack_f16(x0, x1);
+                        const unsigned lo = rest_f16(x0, x1, hi);
+                        if constexpr (G == 8) {
+                            bf[0][u] = transpose8(hi);
+                            bf[1][u] = transpose8(lo);
+                        } else if constexpr (G == 1) {
+                            bf[0][u] = transpose8(__byte_perm(hi, lo, 0x5410));
                         } else {
-                            bf[0][u] = part == 0 ? hi : part == 1 ? mid : part == 2 ? low : 0u;
+                            bf[0][u] = transpose8(rest ? lo : hi);
                         }
                     }
 #pragma unroll
                     for (int k = 2 * g; k < 2 * g + 2; ++k) {
-                        const unsigned a0 = value_bf16<0>(w0[k]), a1 = value_bf16<1>(w0[k]), a2 = value_bf16<0>(w1[k]),
-                                       a3 = value_bf16<1>(w1[k]);
+                        const unsigned a0 = code_f16<0>(w0[k]), a1 = code_f16<1>(w0[k]), a2 = code_f16<0>(w1[k]),
+                                       a3 = code_f16<1>(w1[k]);
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) mma_bf16_16816(acc[2 * k], a0, a1, a2, a3, bf[n][0], bf[n][1]);
-                        const unsigned d0 = value_bf16<2>(w0[k]), d1 = value_bf16<3>(w0[k]), d2 = value_bf16<2>(w1[k]),
-                                       d3 = value_bf16<3>(w1[k]);
+                        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[n][0], bf[n][1]);
+                        const unsigned d0 = code_f16<2>(w0[k]), d1 = code_f16<3>(w0[k]), d2 = code_f16<2>(w1[k]),
+                                       d3 = code_f16<3>(w1[k]);
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) mma_bf16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[n][0], bf[n][1]);
+                        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[n][0], bf[n][1]);
                     }
                 }
-                if ((ring.taken & (AT_FLUSH - 1)) == 0) {
+                if ((ring.taken & (FLUSH - 1)) == 0) {
 #pragma unroll
                     for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -614,17 +638,16 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(FULL, l[e], o);
+            for (int o = 4; o < 32; o <<= 1) {
+                l[e] += __shfl_xor_sync(FULL, l[e], o);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            off[g] += __shfl_xor_sync(FULL, off[g], 1);
-            off[g] += __shfl_xor_sync(FULL, off[g], 2);
-        }
+                for (int g = 0; g < NG; ++g) off[g][e] += __shfl_xor_sync(FULL, off[g][e], o);
+            }
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
         if (r == 0)
 #pragma unroll
             for (int e = 0; e < NE; ++e)
-                if (2 * c + e < min(CP, G)) a.part_ml[slot * G + 2 * c + e] = make_float2(m[e], l[e]);
+                if (2 * c + e < G) a.part_ml[slot * G + 2 * c + e] = make_float2(ref[e], l[e]);
         float *stage = reinterpret_cast<float *>(rings + warp * AT_RING);
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
@@ -633,14 +656,13 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
 #pragma unroll
             for (int v = 0; v < 4; ++v) tot[k][v] += acc[k][v];
 #pragma unroll
-            for (int v = 0; v < 4; v += CP == 1 ? 2 : 1) {
+            for (int v = 0; v < 4; v += G == 1 ? 2 : 1) {
                 float o = tot[k][v];
-                if (CP == 1) o += tot[k][v + 1];
-                if (CP <= 2) o += __shfl_xor_sync(FULL, o, 1);
-                if (CP <= 4) o += __shfl_xor_sync(FULL, o, 2);
+                if (G == 1) o += tot[k][v + 1];
+                if (G == 2) o += __shfl_xor_sync(FULL, o, 1);
+                if (G == 4) o += __shfl_xor_sync(FULL, o, 2);
                 const int n = 2 * c + (v & 1);
-                o += __shfl_sync(FULL, off[k >> 2], 4 * (n % CP));
-                if (n < min(CP, G)) stage[n * D + j + (v >> 1)] = o;
+                if (n < G) stage[n * D + j + (v >> 1)] = o + off[k >> 2][v & 1];
             }
         }
         __syncwarp();
@@ -710,8 +732,8 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     __syncthreads();
     const float nan = __int_as_float(0x7fc00000);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
-    // den is 0 only without tokens (the largest weight of a share is at least
-    // 1); NaN scores make it NaN
+    // den is 0 only without tokens (a share with tokens has a weight of 2^-100
+    // at least); NaN scores make it NaN
     const bool none = den == 0.f;
     if (sub == 0) {
 #pragma unroll
@@ -732,11 +754,11 @@ __global__ void kv4_reset_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     a.zmax[b * a.Hq + h] = ORD_NEG_INF;
 }
 
-template <int D, int CP>
+template <int D, int G>
 __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     using Ring = TileRing<D, false>;
-    constexpr int NE = Queries<D, CP>::NE;
+    constexpr int NE = Queries<D, G>::NE;
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][Ring::NST];
     __shared__ int4 infos[AT_WARPS][Ring::NST];
@@ -745,7 +767,6 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
     if (w >= plan.warps(a)) return;
-    const int G = a.Hq / a.Hkv;
     Ring ring;
     ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
     const size_t row_len = (size_t)a.max_pages * a.P;
@@ -759,14 +780,14 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
         ring.start();
         for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
         const int h0 = sh.b * a.Hq + sh.kvh * G;
-        Queries<D, CP> Q;
-        Q.load(a.q + (size_t)h0 * D, G, (a.alpha - 1.f) * rsqrtf((float)D));
+        Queries<D, G> Q;
+        Q.load(a.q + (size_t)h0 * D, (a.alpha - 1.f) * rsqrtf((float)D));
         const size_t list = (size_t)h0 * row_len + (size_t)sh.first * 16;
 
         float m[2] = {-INFINITY, -INFINITY};      // the share's max so far, of the lane's columns
         float known[2] = {-INFINITY, -INFINITY};  // what other shares of the head have reported
         int next[2] = {ORD_NEG_INF, ORD_NEG_INF};
-        int n[CP] = {};                           // candidates of each head
+        int n[G] = {};                            // candidates of each head
         bool bad[2] = {false, false};             // the lane saw a NaN score
         for (int i = sh.first; i < sh.last; ++i) {
             int4 what;
@@ -785,8 +806,8 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
             float z[4];
             bool any = false;
             if (what.x >= 0) {
-                tile_scores<D, CP>(tile, Q, z);
-                mask_scores<CP>(what, G, z);
+                tile_scores<D, G>(tile, Q, z);
+                mask_scores<G>(what, z);
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     const float thr = fmaxf(m[e], known[e]) - 1.f;
@@ -805,15 +826,14 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
                 for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
                 if (tm > m[e]) {
                     m[e] = tm;
-                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < min(CP, G))
+                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
                         atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
                 }
                 thr[e] = fmaxf(m[e], known[e]) - 1.f;
             }
             const unsigned row = (unsigned)what.x * a.P + 16 * what.w + r;
 #pragma unroll
-            for (int h = 0; h < CP; ++h) {
-                if (h >= G) break;
+            for (int h = 0; h < G; ++h) {
                 const int e = h & 1;
                 const bool mine = c == (h >> 1);
                 const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
@@ -837,11 +857,11 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
         }
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
 #pragma unroll
-        for (int h = 0; h < CP; ++h) {
+        for (int h = 0; h < G; ++h) {
             float mh = __shfl_sync(FULL, m[h & 1], h >> 1);
             // a NaN stays a candidate: its share may not be passed over for a low max
             if (__any_sync(FULL, c == (h >> 1) && bad[h & 1])) mh = __int_as_float(0x7fc00000);
-            if (h < G && lane == 0) a.seg[slot * G + h] = make_int2(n[h], __float_as_int(mh));
+            if (lane == 0) a.seg[slot * G + h] = make_int2(n[h], __float_as_int(mh));
         }
     }
 }
@@ -1052,9 +1072,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         const unsigned char *tile = a.v4 + ((size_t)blk * a.Hkv + kvh) * rec + (size_t)(slot >> 4) * Kv4<D>::TILE;
         // the lane's coordinate block keeps its place: read the word that holds it
         const unsigned w =
-            rotr(__ldg(reinterpret_cast<const unsigned *>(tile) + pair * (D / 4) +
-                       (piece ^ kv4_vswz<D>(pair)) * Kv4<D>::WPL + wi),
-                 3) >>
+            __ldg(reinterpret_cast<const unsigned *>(tile) + pair * (D / 4) +
+                  (piece ^ kv4_vswz<D>(pair)) * Kv4<D>::WPL + wi) >>
             (16 * (t & 1));
         const unsigned pr = __ldg(reinterpret_cast<const unsigned *>(tile + Kv4<D>::CODES) + t * NG + (wi >> 1));
         const float s = p * bf16lo(pr), lo = p * bf16hi(pr);
@@ -1143,19 +1162,19 @@ cudaError_t run_shares(K k, const Kv4DecodeArgs &a, cudaStream_t st) {
     return e != cudaSuccess ? e : launch_pdl(k, dim3(ceil_div(a.W, AT_WARPS)), dim3(AT_THREADS), smem, st, a);
 }
 
-template <int D, int CP>
+template <int D, int G>
 cudaError_t decode_t(const Kv4DecodeArgs &a, cudaStream_t st) {
-    const int heads = a.B * a.nk * (a.Hq / a.Hkv);
+    const int heads = a.B * a.nk * G;
     cudaError_t e;
     if (a.alpha == 1.f) {
-        if ((e = run_shares(kv4_softmax_kernel<D, CP>, a, st)) != cudaSuccess) return e;
+        if ((e = run_shares(kv4_softmax_kernel<D, G>, a, st)) != cudaSuccess) return e;
         return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(CB_NT), (size_t)a.W * 4, st, a);
     }
     if (a.zmax && !a.union_e) {
         e = launch_pdl(kv4_reset_kernel, dim3(ceil_div(heads, 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
-    if ((e = run_shares(kv4_scan_kernel<D, CP>, a, st)) != cudaSuccess) return e;
+    if ((e = run_shares(kv4_scan_kernel<D, G>, a, st)) != cudaSuccess) return e;
     const size_t smem = (size_t)(4 * TK_CAP + a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
@@ -1165,7 +1184,7 @@ cudaError_t decode_t(const Kv4DecodeArgs &a, cudaStream_t st) {
 template <int D>
 cudaError_t decode_d(const Kv4DecodeArgs &a, cudaStream_t st) {
     const int G = a.Hq / a.Hkv;
-    return G == 1 ? decode_t<D, 1>(a, st) : G == 2 ? decode_t<D, 2>(a, st) : G <= 4 ? decode_t<D, 4>(a, st)
+    return G == 1 ? decode_t<D, 1>(a, st) : G == 2 ? decode_t<D, 2>(a, st) : G == 4 ? decode_t<D, 4>(a, st)
                                                                                     : decode_t<D, 8>(a, st);
 }
 

@@ -143,10 +143,9 @@ __device__ __forceinline__ unsigned join_k(const unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     unsigned w;
     if constexpr (D == 128) {
-        const int p = 8 * (lane & 1);
-        w = rotl(kv4_key_pair(c[0], c[1]), p) | rotl(kv4_key_pair(c[2], c[3]), p + 4);
+        w = (c[0] | (c[1] << 16) | (c[2] << 4) | (c[3] << 20)) << (8 * (lane & 1));
     } else {
-        w = rotl(kv4_key_pair(c[0], c[1]), 4 * (lane & 3));
+        w = (c[0] | (c[1] << 16)) << (4 * (lane & 3));
         w |= __shfl_xor_sync(FULL, w, 2);
     }
     return w | __shfl_xor_sync(FULL, w, 1);
@@ -166,22 +165,22 @@ template <int D>
 __device__ __forceinline__ void split_k(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     if constexpr (D == 128) {
-        const unsigned w = rotr(tile[kv4_kword<D>(t, lane >> 1)], 8 * (lane & 1)), x = rotr(w, 4);
-        c[0] = kv4_key_code(w);
-        c[1] = kv4_key_code(w >> 16);
-        c[2] = kv4_key_code(x);
-        c[3] = kv4_key_code(x >> 16);
+        const unsigned w = tile[kv4_kword<D>(t, lane >> 1)] >> (8 * (lane & 1));
+        c[0] = w & 15;
+        c[1] = (w >> 16) & 15;
+        c[2] = (w >> 4) & 15;
+        c[3] = (w >> 20) & 15;
     } else {
-        const unsigned w = rotr(tile[kv4_kword<D>(t, lane >> 2)], 4 * (lane & 3));
-        c[0] = kv4_key_code(w);
-        c[1] = kv4_key_code(w >> 16);
+        const unsigned w = tile[kv4_kword<D>(t, lane >> 2)] >> (4 * (lane & 3));
+        c[0] = w & 15;
+        c[1] = (w >> 16) & 15;
     }
 }
 template <int D>
 __device__ __forceinline__ void split_v(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
     const int lane = threadIdx.x & 31;
     const int q4 = D == 128 ? lane : lane >> 1;
-    unsigned w = rotr(tile[kv4_vword<D>(t >> 1, q4)], 3) >> (16 * (t & 1));
+    unsigned w = tile[kv4_vword<D>(t >> 1, q4)] >> (16 * (t & 1));
     if constexpr (D == 64) w >>= 8 * (lane & 1);
 #pragma unroll
     for (int i = 0; i < CPL<D>; ++i) c[i] = (w >> (4 * i)) & 15;
@@ -285,10 +284,10 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_cons
             unsigned *w = reinterpret_cast<unsigned *>(vtile) + kv4_vword<D>((t & 15) >> 1, lane / SH);
             unsigned v = half[0] | (half[1] << 16);
             if (!(has0 && has1)) {  // the other token of the pair keeps its half
-                const unsigned old = rotr(*w, 3);
+                const unsigned old = *w;
                 v = has0 ? (half[0] | (old & 0xffff0000u)) : ((half[1] << 16) | (old & 0xffffu));
             }
-            *w = rotl(v, 3);
+            *w = v;
         }
     }
     if (!meta) return;

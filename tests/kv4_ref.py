@@ -56,14 +56,8 @@ def pack_tile(c, s, lo, values_layout):
             else:
                 w = t * (d // 8) + (r // 16) * (d // 32) + 2 * g + (r // 8) % 2
                 n = r % 8
-                k, x = 16 * (n & 1) + 4 * (n >> 1), 2 * int(c[t, j]) - 15
-                words[w] |= np.uint64((x < 0) << (15 + k) % 32)
-                for i in range(3):
-                    words[w] |= np.uint64((((abs(x) - 1) // 2 >> i) & 1) << (4 + i + k) % 32)
-                continue
+                bit = 16 * (n & 1) + 4 * (n >> 1)
             words[w] |= np.uint64(int(c[t, j]) << bit)
-    if values_layout:
-        words = ((words << np.uint64(3)) | (words >> np.uint64(29))) & np.uint64(0xFFFFFFFF)
     params = _bits16(s) | (_bits16(lo) << 16)
     return np.concatenate([words.astype("<u4").view(np.uint8), params.reshape(-1).astype("<u4").view(np.uint8)])
 
@@ -74,10 +68,6 @@ def code_mask(d, tokens, values_layout):
     c[tokens] = 15
     z = np.zeros((16, d // 64))
     m = pack_tile(c, z, z, values_layout)
-    if not values_layout:  # a key's words are its own
-        words = m[:8 * d].view("<u4").reshape(16, -1)
-        words[:] = 0
-        words[tokens] = 0xFFFFFFFF
     par = m[8 * d:].view("<u4").reshape(16, -1)
     par[tokens] = 0xFFFFFFFF
     return m
