@@ -24,11 +24,11 @@
 //           set of fp32 registers every few tiles, so that few truncations
 //           meet a large sum.
 //
-// The tiles (16 tokens of one kv head) of all groups' page lists form one
+// The chunks (16 or 32 tokens of one kv head) of all groups' page lists form one
 // range that is cut evenly among the warps of a grid that fills the GPU once:
 // ragged batches and any number of groups keep every SM busy to the end.  A
-// warp takes its tiles through a ring of its own in shared memory, filled by
-// bulk copies several tiles ahead, and reads each tile once for all query
+// warp takes its chunks through a ring of its own in shared memory, filled by
+// bulk copies ahead of use, and reads each 16-token tile once for all query
 // heads of the group (heads are the n dimension of m16n8k16, tokens or value
 // coordinates the m dimension).
 //   softmax  running max, sum and output per head, one partial for each warp
@@ -51,12 +51,16 @@ namespace {
 
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
-constexpr int AT_RING = 9216;           // bytes of a warp's ring
 constexpr int AT_MAX_WARPS = 148 * 5 * AT_WARPS;
-constexpr int AT_MIN_TILES = 2;         // tiles a warp gets at least ...
+constexpr int AT_MIN_CHUNKS = 2;        // chunks a warp gets at least ...
 constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
 constexpr float AT_MAX_X = 32768.f;     // p s stays below this (fp16 ends at 65504) ...
 constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a reference is set
+
+// CTAs an SM holds (registers bound the softmax, shared memory allows five).
+template <int D, int G>
+constexpr int softmax_ctas() { return D == 64 && G < 8 ? 4 : 3; }
+constexpr int SCAN_CTAS = 5;
 
 struct Kv4DecodeArgs {
     const uint16_t *q;
@@ -71,14 +75,15 @@ struct Kv4DecodeArgs {
     int2 *seg;            // [slots][G] candidates of a warp's share of a group, their max
     int *zmax;            // [B Hq] running max of a head's z (order-mapped), null: none kept
     int W;                // warps that share the tiles at most
-    int B, Hq, Hkv, P, lp, max_pages, num_blocks;
+    int ct, lc;           // tiles of a chunk (1 or 2), log2 of the chunks of a page
+    int B, Hq, Hkv, P, max_pages, num_blocks;
     int kv0, nk;
     float alpha;
     int r_int;
     int *status;
 };
 
-// --------------------------------------------------------------- the range of tiles
+// --------------------------------------------------------------- the range of chunks
 
 // Entries of the range: the sequences (nk groups each), or the groups of the
 // selections' unions.
@@ -87,16 +92,16 @@ __device__ __forceinline__ int tokens_of(const Kv4DecodeArgs &a, int b) {
     const int s = __ldg(a.seq_lens + b), cap = a.max_pages * a.P;
     return s < 0 ? 0 : min(s, cap);
 }
-// Tiles of each group of entry i.
-__device__ __forceinline__ int entry_tiles(const Kv4DecodeArgs &a, int i) {
-    if (!a.union_e) return n_pages_of(tokens_of(a, i), a.P) << a.lp;
+// Chunks of each group of entry i.
+__device__ __forceinline__ int entry_chunks(const Kv4DecodeArgs &a, int i) {
+    if (!a.union_e) return n_pages_of(tokens_of(a, i), a.P) << a.lc;
     int b, kvh;
     group_of(i, a.kv0, a.nk, b, kvh);
-    return __ldg(a.union_cnt + b * a.Hkv + kvh) << a.lp;
+    return __ldg(a.union_cnt + b * a.Hkv + kvh) << a.lc;
 }
 __device__ __forceinline__ int groups_of_entry(const Kv4DecodeArgs &a) { return a.union_e ? 1 : a.nk; }
 
-// Tiles before the entries of each thread of the CTA (thread i owns entries
+// Chunks before the entries of each thread of the CTA (thread i owns entries
 // i C .. i C + C - 1), and their total.
 template <int NT>
 struct Plan {
@@ -106,7 +111,7 @@ struct Plan {
         const int n = n_entries(a), C = (n + NT - 1) / NT, m = groups_of_entry(a);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         long long v = 0;
-        for (int i = threadIdx.x * C; i < min(n, (int)(threadIdx.x + 1) * C); ++i) v += (long long)entry_tiles(a, i) * m;
+        for (int i = threadIdx.x * C; i < min(n, (int)(threadIdx.x + 1) * C); ++i) v += (long long)entry_chunks(a, i) * m;
         long long x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -121,14 +126,14 @@ struct Plan {
         __syncthreads();
     }
     __device__ long long total() const { return pre[NT]; }
-    // Warps that share the range: no more than its tiles, so that none is left without.
+    // Warps that share the range: no more than its chunks, so that none is left without.
     __device__ int warps(const Kv4DecodeArgs &a) const { return (int)min((long long)a.W, total()); }
     __device__ long long first_of(const Kv4DecodeArgs &a, int w) const { return total() * w / warps(a); }
-    // First tile of entry i.
+    // First chunk of entry i.
     __device__ long long start_of(const Kv4DecodeArgs &a, int i) const {
         const int C = (n_entries(a) + NT - 1) / NT, m = groups_of_entry(a);
         long long s = pre[i / C];
-        for (int k = i / C * C; k < i; ++k) s += (long long)entry_tiles(a, k) * m;
+        for (int k = i / C * C; k < i; ++k) s += (long long)entry_chunks(a, k) * m;
         return s;
     }
 };
@@ -137,14 +142,14 @@ struct Plan {
 struct Share {
     int b, kvh, bk, g;  // g: group in the order of the range
     int U, seq;         // pages of the list, tokens of the sequence
-    int first, last;    // tiles [first, last) of the list
+    int first, last;    // chunks [first, last) of the list
 };
 
-// Walks the entries from tile t on.
+// Walks the entries from chunk t on.
 struct Walk {
     int i;            // entry
-    int T;            // tiles of each of its groups
-    long long start;  // its first tile
+    int T;            // chunks of each of its groups
+    long long start;  // its first chunk
     template <int NT>
     __device__ void to(const Kv4DecodeArgs &a, const Plan<NT> &p, long long t) {
         int lo = 0, hi = NT - 1;
@@ -155,20 +160,20 @@ struct Walk {
         }
         start = p.pre[lo];
         i = lo * ((n_entries(a) + NT - 1) / NT);
-        T = entry_tiles(a, i);
+        T = entry_chunks(a, i);
     }
     __device__ Share share(const Kv4DecodeArgs &a, long long t, long long end) {
         const int m = groups_of_entry(a);
         while (start + (long long)T * m <= t) {
             start += (long long)T * m;
-            T = entry_tiles(a, ++i);
+            T = entry_chunks(a, ++i);
         }
         const int sub = (int)((t - start) / T);
         Share s;
         s.g = i * m + sub;
         group_of(s.g, a.kv0, a.nk, s.b, s.kvh);
         s.bk = s.b * a.Hkv + s.kvh;
-        s.U = T >> a.lp;
+        s.U = T >> a.lc;
         s.seq = tokens_of(a, s.b);
         const long long at = start + (long long)sub * T;
         s.first = (int)(t - at);
@@ -188,7 +193,7 @@ __device__ GroupSlots group_slots(const Kv4DecodeArgs &a, const Plan<NT> &p, int
     GroupSlots r;
     r.g = b * a.nk + kvh - a.kv0;
     const int i = a.union_e ? r.g : b;
-    const int T = entry_tiles(a, i);
+    const int T = entry_chunks(a, i);
     r.w0 = 0;
     r.w1 = -1;
     if (T == 0) return r;
@@ -204,79 +209,103 @@ __host__ __device__ inline size_t slots_per_head(int B) { return (size_t)AT_MAX_
 
 // --------------------------------------------------------------- the ring of tiles
 
-// A stage: the key tile (and the value tile), and what it holds.
+// A stage holds a chunk: the one or two tiles (16 or 32 tokens) of a page that
+// lie together, of the keys (and behind them of the values).
+constexpr int RING_STAGES = 3;
 template <int D, bool BOTH>
 struct TileRing {
-    static constexpr int STAGE = Kv4<D>::TILE * (BOTH ? 2 : 1);
-    static constexpr int NST = AT_RING / STAGE > 8 ? 8 : AT_RING / STAGE;  // a power of two: 4 or 8
-    static_assert((NST & (NST - 1)) == 0, "stages");
+    static constexpr int HALF = 2 * Kv4<D>::TILE;
+    static constexpr int STAGE = HALF * (BOTH ? 2 : 1);
+    static constexpr int BYTES = RING_STAGES * STAGE;
     unsigned char *base;
     uint64_t *bar;
-    int4 *info;  // block (-1: nothing to read), valid tokens, head mask, tile of the page
-    unsigned issued = 0, taken = 0;
-    int e0 = 0, ent = 0, blk = 0;  // the lane's entry of 32 list entries from e0 on
+    int2 *info;              // first cache row (block P + slot); valid tokens, and the head mask << 8
+    int in = 0, out = 0;     // stages to fill and to take next
+    unsigned parity = 0;     // of the stage to take
+    int flying = 0;          // filled, not taken
+    int e0 = 0;              // the lane's entry of 32 list entries from e0 on:
+    int row = 0, tokens = 0, mask = 0;
+    size_t at = 0;           // its byte offset in the cache
 
-    __device__ __forceinline__ void init(unsigned char *b, uint64_t *bars, int4 *i) {
+    __device__ __forceinline__ void init(unsigned char *b, uint64_t *bars, int2 *i) {
         base = b;
         bar = bars;
         info = i;
         if ((threadIdx.x & 31) == 0) {
-            for (int s = 0; s < NST; ++s) mbar_init(&bar[s], 1);
+            for (int s = 0; s < RING_STAGES; ++s) mbar_init(&bar[s], 1);
             mbar_fence_init();
         }
         __syncwarp();
     }
     __device__ __forceinline__ void start() { e0 = -(1 << 30); }  // a new list
-    __device__ __forceinline__ void issue(const Kv4DecodeArgs &a, const Share &s, int tile) {
-        const int lane = threadIdx.x & 31;
-        const int e = tile >> a.lp;
-        if (e - e0 >= 32 || e < e0) {
-            e0 = e;
-            const int i = e + lane;
-            ent = 0;
-            blk = -1;
-            if (i < s.U) {
-                if (a.union_e) {
-                    ent = __ldg(a.union_e + (size_t)s.bk * a.max_pages + i);
-                    blk = __ldg(a.union_blk + (size_t)s.bk * a.max_pages + i);
-                } else {
-                    blk = __ldg(a.page_table + (size_t)s.b * a.max_pages + i);
-                    if (blk < 0 || blk >= a.num_blocks) {
-                        atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
-                        blk = -1;
-                    }
-                }
+    __device__ __forceinline__ void window(const Kv4DecodeArgs &a, const Share &s, int e) {
+        const int i = e + (threadIdx.x & 31);
+        e0 = e;
+        tokens = 0;
+        if (i >= s.U) return;
+        int page = i, blk;
+        mask = 0xff;
+        if (a.union_e) {
+            const int ent = __ldg(a.union_e + (size_t)s.bk * a.max_pages + i);
+            blk = __ldg(a.union_blk + (size_t)s.bk * a.max_pages + i);
+            page = ent >> 8;
+            mask = ent & 0xff;
+        } else {
+            blk = __ldg(a.page_table + (size_t)s.b * a.max_pages + i);
+            if (blk < 0 || blk >= a.num_blocks) atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
+        }
+        if (blk < 0 || blk >= a.num_blocks) return;
+        tokens = min(a.P, s.seq - page * a.P);
+        row = (unsigned)blk * a.P;
+        at = kv4_tile<D>(blk, a.Hkv, s.kvh, a.P, 0);
+    }
+    // Starts the copy of a chunk of the list into the next free stage.
+    __device__ __forceinline__ void issue(const Kv4DecodeArgs &a, const Share &s, int chunk) {
+        const int e = chunk >> a.lc;
+        if ((unsigned)(e - e0) >= 32u) window(a, s, e);
+        if ((int)(threadIdx.x & 31) == e - e0) {  // the lane that has the entry
+            const int t16 = (chunk & ((1 << a.lc) - 1)) * a.ct;
+            const int nval = max(0, min(16 * a.ct, tokens - 16 * t16));
+            info[in] = make_int2(row + 16 * t16, nval | (mask << 8));
+            if (nval > 0) {
+                const unsigned bytes = a.ct * Kv4<D>::TILE;
+                const size_t o = at + t16 * Kv4<D>::TILE;
+                unsigned char *dst = base + in * STAGE;
+                mbar_arrive_expect_tx(&bar[in], bytes * (BOTH ? 2 : 1));
+                bulk_g2s(dst, a.k4 + o, bytes, &bar[in]);
+                if (BOTH) bulk_g2s(dst + HALF, a.v4 + o, bytes, &bar[in]);
+            } else {
+                mbar_arrive(&bar[in]);
             }
         }
-        const int en = __shfl_sync(FULL, ent, e - e0), bl = __shfl_sync(FULL, blk, e - e0);
-        const int st = issued++ % NST;
-        if (lane == 0) {
-            const int t16 = tile & ((1 << a.lp) - 1);
-            const int nval = min(16, s.seq - (a.union_e ? en >> 8 : e) * a.P - 16 * t16);
-            const bool has = bl >= 0 && nval > 0;
-            info[st] = make_int4(has ? bl : -1, nval, a.union_e ? en & 0xff : 0xff, t16);
-            if (has) {
-                const size_t at = kv4_tile<D>(bl, a.Hkv, s.kvh, a.P, t16);
-                mbar_arrive_expect_tx(&bar[st], STAGE);
-                bulk_g2s(base + st * STAGE, a.k4 + at, Kv4<D>::TILE, &bar[st]);
-                if (BOTH) bulk_g2s(base + st * STAGE + Kv4<D>::TILE, a.v4 + at, Kv4<D>::TILE, &bar[st]);
-            } else {
-                mbar_arrive(&bar[st]);
-            }
+        in = in == RING_STAGES - 1 ? 0 : in + 1;
+        ++flying;
+    }
+    __device__ __forceinline__ bool wait(const Kv4DecodeArgs &a) {
+        const bool ok = mbar_wait(&bar[out], parity, a.status);
+        --flying;
+        return ok;
+    }
+    __device__ __forceinline__ void pass() {
+        if (++out == RING_STAGES) {
+            out = 0;
+            parity ^= 1u;
         }
     }
     // Waits for the next stage.  False: it did not come (the status word says so).
-    __device__ __forceinline__ bool take(const Kv4DecodeArgs &a, int4 &what, unsigned char *&tile) {
-        const int st = taken % NST;
-        const bool ok = mbar_wait(&bar[st], (taken / NST) & 1, a.status);
-        ++taken;
-        what = info[st];
-        tile = base + st * STAGE;
+    __device__ __forceinline__ bool take(const Kv4DecodeArgs &a, int2 &what, unsigned char *&tile) {
+        const bool ok = wait(a);
+        what = info[out];
+        tile = base + out * STAGE;
+        pass();
         return __all_sync(FULL, ok);
     }
     // After a wait that ran out: the copies in flight have to land before the CTA ends.
-    __device__ void drain(const Kv4DecodeArgs &a) {
-        for (; taken < issued; ++taken) mbar_wait(&bar[taken % NST], (taken / NST) & 1, a.status);
+    __device__ __forceinline__ void drain(const Kv4DecodeArgs &a) {
+        while (flying > 0) {
+            wait(a);
+            pass();
+        }
     }
 };
 
@@ -450,33 +479,39 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
     for (int v = 0; v < 4; ++v)
         if ((v & 1) < NE) z[v] *= Q.factor[v & 1 & (NE - 1)];
 }
-// Whether head n % G of the group selected the page of the tile.
+// Whether head n % G of the group selected the page, and whether all its heads
+// see all tokens of a tile that has n valid ones.
 template <int G>
-__device__ __forceinline__ bool keeps(const int4 &what, int n) { return (what.z >> (n % G)) & 1; }
+__device__ __forceinline__ bool keeps(int mask, int n) { return (mask >> (n % G)) & 1; }
 template <int G>
-__device__ __forceinline__ bool whole(const int4 &what) { return what.y >= 16 && (~what.z & ((1 << G) - 1)) == 0; }
+__device__ __forceinline__ bool whole(int mask, int n) { return n >= 16 && (~mask & ((1 << G) - 1)) == 0; }
 // Tokens behind the sequence and heads that did not select the page: -inf.
 template <int G>
-__device__ __forceinline__ void mask_scores(const int4 &what, float (&z)[4]) {
+__device__ __forceinline__ void mask_scores(int mask, int n, float (&z)[4]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    if (whole<G>(what)) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-        if (r + 8 * (v >> 1) >= what.y || !keeps<G>(what, 2 * c + (v & 1))) z[v] = -INFINITY;
+        if (r + 8 * (v >> 1) >= n || !keeps<G>(mask, 2 * c + (v & 1))) z[v] = -INFINITY;
 }
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
 
 // -------------------------------------------------------------- softmax
 
 template <int D, int G>
-__global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, G>::NE;
     constexpr int NB = G == 8 ? 2 : 1;  // products per value operand: both parts, or both in one
     constexpr int FLUSH = 8 / NB;       // tiles between flushes of the output sums
     using Ring = TileRing<D, true>;
     extern __shared__ __align__(128) unsigned char rings[];
-    __shared__ uint64_t bars[AT_WARPS][Ring::NST];
-    __shared__ int4 infos[AT_WARPS][Ring::NST];
+    __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
+    __shared__ int2 infos[AT_WARPS][RING_STAGES];
     __shared__ Plan<AT_THREADS> plan;
     plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -484,7 +519,7 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
     if (w >= plan.warps(a)) return;
     const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
-    ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
+    ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     long long t = plan.first_of(a, w);
     const long long end = plan.first_of(a, w + 1);
     Walk walk;
@@ -493,7 +528,7 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
         const Share sh = walk.share(a, t, end);
         t += sh.last - sh.first;
         ring.start();
-        for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
         Queries<D, G> Q;
         // z in powers of two
         Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, 1.4426950408889634f * rsqrtf((float)D));
@@ -506,45 +541,57 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
         // per column of the lane: the reference (weights are 2^(z - ref)), the
         // sums of p and of p (lo + 8 s) over the lane's tokens
         float ref[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, off[NG][2] = {};
+        int until = FLUSH;
         for (int i = sh.first; i < sh.last; ++i) {
-            int4 what;
-            unsigned char *tile;
-            if (!ring.take(a, what, tile)) {
+            int2 what;
+            unsigned char *stage;
+            if (!ring.take(a, what, stage)) {
                 ring.drain(a);
                 return;
             }
-            if (what.x >= 0) {
-                float z[4], p[4], x[NG][4];
+            const int mask = what.y >> 8;
+            int n = what.y & 0xff;
+#pragma unroll 1
+            for (const unsigned char *tile = stage; n > 0; n -= 16, tile += Kv4<D>::TILE) {
+                float z[4], p[4], x[NG][4], y[NG][2];
                 tile_scores<D, G>(tile, Q, z);
-                mask_scores<G>(what, z);
-                const unsigned char *vt = tile + Kv4<D>::TILE;
+                const unsigned char *vt = tile + Ring::HALF;
                 Params<D> P;
                 P.load(vt);
-                const bool all = whole<G>(what);
-                if (!all) {  // rows behind the sequence may hold anything
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if (r + 8 * u >= what.y)
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) P.s[u][g] = P.o[u][g] = 0.f;
-                }
-                auto weights = [&] {
+                // weights p, the x = p s, and y, the sums of p (lo + 8 s)
+                auto weights = [&](auto masked) {
                     float sum = 0.f;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        if ((v & 1) >= NE) continue;
-                        p[v] = ex2(z[v] - ref[v & 1]);
+                    for (int e = 0; e < NE; ++e) {
+                        p[e] = ex2(z[e] - ref[e]);
+                        p[2 + e] = ex2(z[2 + e] - ref[e]);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
-                            x[g][v] = p[v] * P.s[v >> 1][g];
-                            // so may pages of other heads
-                            if (!all && !keeps<G>(what, 2 * c + (v & 1))) x[g][v] = 0.f;
-                            sum += x[g][v];
+                            x[g][e] = p[e] * P.s[0][g];
+                            x[g][2 + e] = p[2 + e] * P.s[1][g];
+                            y[g][e] = fmaf(p[e], P.o[0][g], p[2 + e] * P.o[1][g]);
+                            // pages that the head did not select may hold anything
+                            if (masked.value && !keeps<G>(mask, 2 * c + e)) x[g][e] = x[g][2 + e] = y[g][e] = 0.f;
+                            sum += x[g][e] + x[g][2 + e];
                         }
                     }
                     return sum;
                 };
-                if (__any_sync(FULL, !(weights() <= AT_MAX_X))) {
+                float sum;
+                const bool all = whole<G>(mask, n);
+                if (all) {
+                    sum = weights(No{});
+                } else {
+                    mask_scores<G>(mask, n, z);
+                    // so may rows behind the sequence
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (r + 8 * u >= n)
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) P.s[u][g] = P.o[u][g] = 0.f;
+                    sum = weights(Yes{});
+                }
+                if (__any_sync(FULL, !(sum <= AT_MAX_X))) {
                     // the reference follows the largest p s
                     float corr[2] = {1.f, 1.f};
 #pragma unroll
@@ -574,17 +621,13 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                             acc[k][v] *= corr[v & 1];
                             tot[k][v] *= corr[v & 1];
                         }
-                    weights();
+                    weights(Yes{});
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     l[e] += p[e] + p[2 + e];
-                    const bool kept = all || keeps<G>(what, 2 * c + e);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const float y = fmaf(p[e], P.o[0][g], fmaf(p[2 + e], P.o[1][g], off[g][e]));
-                        if (kept) off[g][e] = y;
-                    }
+                    for (int g = 0; g < NG; ++g) off[g][e] += y[g][e];
                 }
                 unsigned w0[WPL], w1[WPL];
                 const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
@@ -613,14 +656,15 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                         const unsigned a0 = code_f16<0>(w0[k]), a1 = code_f16<1>(w0[k]), a2 = code_f16<0>(w1[k]),
                                        a3 = code_f16<1>(w1[k]);
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[n][0], bf[n][1]);
+                        for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[q][0], bf[q][1]);
                         const unsigned d0 = code_f16<2>(w0[k]), d1 = code_f16<3>(w0[k]), d2 = code_f16<2>(w1[k]),
                                        d3 = code_f16<3>(w1[k]);
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[n][0], bf[n][1]);
+                        for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[q][0], bf[q][1]);
                     }
                 }
-                if ((ring.taken & (FLUSH - 1)) == 0) {
+                if (--until == 0) {
+                    until = FLUSH;
 #pragma unroll
                     for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -631,7 +675,7 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                 }
             }
             __syncwarp();
-            if (i + Ring::NST < sh.last) ring.issue(a, sh, i + Ring::NST);
+            if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
         }
         // the share's partial: sums over the lanes of a column and over the
         // columns of a head, through the ring's memory (no copy is in flight)
@@ -648,7 +692,7 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < NE; ++e)
                 if (2 * c + e < G) a.part_ml[slot * G + 2 * c + e] = make_float2(ref[e], l[e]);
-        float *stage = reinterpret_cast<float *>(rings + warp * AT_RING);
+        float *merge = reinterpret_cast<float *>(ring.base);
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
             // tile k holds coordinates j (row r) and j + 1 (row r + 8)
@@ -662,13 +706,13 @@ __global__ void __launch_bounds__(AT_THREADS, 3) kv4_softmax_kernel(const __grid
                 if (G == 2) o += __shfl_xor_sync(FULL, o, 1);
                 if (G == 4) o += __shfl_xor_sync(FULL, o, 2);
                 const int n = 2 * c + (v & 1);
-                if (n < G) stage[n * D + j + (v >> 1)] = o + off[k >> 2][v & 1];
+                if (n < G) merge[n * D + j + (v >> 1)] = o + off[k >> 2][v & 1];
             }
         }
         __syncwarp();
         for (int i = lane; i < G * D / 4; i += 32)
-            reinterpret_cast<float4 *>(a.part_o + slot * G * D)[i] = reinterpret_cast<const float4 *>(stage)[i];
-        // the next share's copies write over the stage
+            reinterpret_cast<float4 *>(a.part_o + slot * G * D)[i] = reinterpret_cast<const float4 *>(merge)[i];
+        // the next share's copies write over it
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
     }
@@ -755,20 +799,20 @@ __global__ void kv4_reset_kernel(const __grid_constant__ Kv4DecodeArgs a) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     using Ring = TileRing<D, false>;
     constexpr int NE = Queries<D, G>::NE;
     extern __shared__ __align__(128) unsigned char rings[];
-    __shared__ uint64_t bars[AT_WARPS][Ring::NST];
-    __shared__ int4 infos[AT_WARPS][Ring::NST];
+    __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
+    __shared__ int2 infos[AT_WARPS][RING_STAGES];
     __shared__ Plan<AT_THREADS> plan;
     plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
     if (w >= plan.warps(a)) return;
     Ring ring;
-    ring.init(rings + warp * AT_RING, bars[warp], infos[warp]);
+    ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     const size_t row_len = (size_t)a.max_pages * a.P;
     long long t = plan.first_of(a, w);
     const long long end = plan.first_of(a, w + 1);
@@ -778,82 +822,83 @@ __global__ void __launch_bounds__(AT_THREADS, 5) kv4_scan_kernel(const __grid_co
         const Share sh = walk.share(a, t, end);
         t += sh.last - sh.first;
         ring.start();
-        for (int i = 0; i < Ring::NST && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
         const int h0 = sh.b * a.Hq + sh.kvh * G;
         Queries<D, G> Q;
         Q.load(a.q + (size_t)h0 * D, (a.alpha - 1.f) * rsqrtf((float)D));
-        const size_t list = (size_t)h0 * row_len + (size_t)sh.first * 16;
+        const size_t list = (size_t)h0 * row_len + (size_t)sh.first * (16 * a.ct);
 
         float m[2] = {-INFINITY, -INFINITY};      // the share's max so far, of the lane's columns
         float known[2] = {-INFINITY, -INFINITY};  // what other shares of the head have reported
         int next[2] = {ORD_NEG_INF, ORD_NEG_INF};
+        float thr[2] = {-INFINITY, -INFINITY};    // below it a score carries no weight
         int n[G] = {};                            // candidates of each head
         bool bad[2] = {false, false};             // the lane saw a NaN score
         for (int i = sh.first; i < sh.last; ++i) {
-            int4 what;
-            unsigned char *tile;
-            if (!ring.take(a, what, tile)) {
+            int2 what;
+            unsigned char *stage;
+            if (!ring.take(a, what, stage)) {
                 ring.drain(a);
                 return;
             }
-            if (a.zmax && (ring.taken & 3) == 1) {  // used four tiles on: nothing waits for the load
+            if (a.zmax && (i & 1)) {  // used two chunks on: nothing waits for the load
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     known[e] = fmaxf(known[e], ord2f(next[e]));
+                    thr[e] = fmaxf(m[e], known[e]) - 1.f;
                     if (2 * c + e < G) next[e] = __ldcg(a.zmax + h0 + 2 * c + e);
                 }
             }
-            float z[4];
-            bool any = false;
-            if (what.x >= 0) {
+            const int mask = what.y >> 8;
+            int left = what.y & 0xff;
+            unsigned row = (unsigned)what.x + r;
+#pragma unroll 1
+            for (const unsigned char *tile = stage; left > 0; left -= 16, tile += Kv4<D>::TILE, row += 16) {
+                float z[4];
                 tile_scores<D, G>(tile, Q, z);
-                mask_scores<G>(what, z);
+                if (!whole<G>(mask, left)) mask_scores<G>(mask, left, z);
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) any |= !(z[e] <= thr[e]) || !(z[2 + e] <= thr[e]);  // NaN stays a candidate
+                if (!__any_sync(FULL, any)) continue;
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float thr = fmaxf(m[e], known[e]) - 1.f;
-                    any |= !(z[e] <= thr) || !(z[2 + e] <= thr);  // NaN stays a candidate
+                    bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
+                    float tm = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
+                    if (tm > m[e]) {
+                        m[e] = tm;
+                        if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
+                            atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
+                    }
+                    thr[e] = fmaxf(m[e], known[e]) - 1.f;
+                }
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    const int e = h & 1;
+                    const bool mine = c == (h >> 1);
+                    const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
+                    const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
+                    if (lo | hi) {
+                        const size_t at = list + h * row_len + n[h];
+                        const unsigned below = (1u << lane) - 1u;
+                        if ((lo >> lane) & 1u) {
+                            const size_t k = at + __popc(lo & below);
+                            a.cand_z[k] = z[e];
+                            a.cand_row[k] = row;
+                        }
+                        if ((hi >> lane) & 1u) {
+                            const size_t k = at + __popc(lo) + __popc(hi & below);
+                            a.cand_z[k] = z[2 + e];
+                            a.cand_row[k] = row + 8;
+                        }
+                        n[h] += __popc(lo) + __popc(hi);
+                    }
                 }
             }
             __syncwarp();
-            if (i + Ring::NST < sh.last) ring.issue(a, sh, i + Ring::NST);
-            if (!__any_sync(FULL, any)) continue;
-            float thr[2];
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
-                float tm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
-                if (tm > m[e]) {
-                    m[e] = tm;
-                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
-                        atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
-                }
-                thr[e] = fmaxf(m[e], known[e]) - 1.f;
-            }
-            const unsigned row = (unsigned)what.x * a.P + 16 * what.w + r;
-#pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const int e = h & 1;
-                const bool mine = c == (h >> 1);
-                const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
-                const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
-                if (lo | hi) {
-                    const size_t at = list + h * row_len + n[h];
-                    const unsigned below = (1u << lane) - 1u;
-                    if ((lo >> lane) & 1u) {
-                        const size_t k = at + __popc(lo & below);
-                        a.cand_z[k] = z[e];
-                        a.cand_row[k] = row;
-                    }
-                    if ((hi >> lane) & 1u) {
-                        const size_t k = at + __popc(lo) + __popc(hi & below);
-                        a.cand_z[k] = z[2 + e];
-                        a.cand_row[k] = row + 8;
-                    }
-                    n[h] += __popc(lo) + __popc(hi);
-                }
-            }
+            if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
         }
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
 #pragma unroll
@@ -930,7 +975,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
     // first place of a share's list in the head's
-    auto seg_base = [&](int w) { return (int)max(0ll, plan.first_of(a, gs.w0 + w) - gs.start) * 16; };
+    auto seg_base = [&](int w) { return (int)max(0ll, plan.first_of(a, gs.w0 + w) - gs.start) * (16 * a.ct); };
     // listed candidates of a share that reaches the cut
     auto seg_size = [&](int w) {
         const int2 s = __ldcg(seg + (size_t)w * G);
@@ -1113,16 +1158,16 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 
 // --------------------------------------------------------------- launch
 
-// Warps that share the tiles of a call over nk kv heads, on `ctas` CTAs an SM:
-// the grid fills the GPU once, unless that leaves fewer than AT_MIN_TILES
-// tiles to a warp or cuts each group's list in more than AT_GROUP_PARTS.
-int share_warps(const entmaxkv_shape *s, int nk, int sms, int ctas) {
-    const long long groups = (long long)s->B * nk;
-    const long long tiles = groups * s->max_pages * (s->page_size / 16);
+// Warps that share the chunks of a call over nk kv heads, on `ctas` CTAs an SM:
+// the grid fills the GPU once, unless that leaves fewer than AT_MIN_CHUNKS
+// chunks to a warp or cuts each group's list in more than AT_GROUP_PARTS.
+int share_warps(const Kv4DecodeArgs &a, int sms, int ctas) {
+    const long long groups = (long long)a.B * a.nk;
+    const long long chunks = (groups * a.max_pages) << a.lc;
     long long W = (long long)sms * ctas * AT_WARPS;
     if (W > AT_MAX_WARPS) W = AT_MAX_WARPS;
     if (W > groups * AT_GROUP_PARTS) W = groups * AT_GROUP_PARTS;
-    if (W > (tiles + AT_MIN_TILES - 1) / AT_MIN_TILES) W = (tiles + AT_MIN_TILES - 1) / AT_MIN_TILES;
+    if (W > (chunks + AT_MIN_CHUNKS - 1) / AT_MIN_CHUNKS) W = (chunks + AT_MIN_CHUNKS - 1) / AT_MIN_CHUNKS;
     return (int)W;
 }
 
@@ -1156,25 +1201,29 @@ Carve carve(const entmaxkv_shape *s) {
 }
 
 template <class K>
-cudaError_t run_shares(K k, const Kv4DecodeArgs &a, cudaStream_t st) {
-    const size_t smem = (size_t)AT_WARPS * AT_RING;
+cudaError_t run_shares(K k, const Kv4DecodeArgs &a, size_t smem, cudaStream_t st) {
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k), smem);
     return e != cudaSuccess ? e : launch_pdl(k, dim3(ceil_div(a.W, AT_WARPS)), dim3(AT_THREADS), smem, st, a);
 }
 
 template <int D, int G>
-cudaError_t decode_t(const Kv4DecodeArgs &a, cudaStream_t st) {
+cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
     const int heads = a.B * a.nk * G;
     cudaError_t e;
     if (a.alpha == 1.f) {
-        if ((e = run_shares(kv4_softmax_kernel<D, G>, a, st)) != cudaSuccess) return e;
+        a.W = share_warps(a, sms, softmax_ctas<D, G>());
+        e = run_shares(kv4_softmax_kernel<D, G>, a, AT_WARPS * TileRing<D, true>::BYTES, st);
+        if (e != cudaSuccess) return e;
         return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(CB_NT), (size_t)a.W * 4, st, a);
     }
+    a.W = share_warps(a, sms, SCAN_CTAS);
+    // short shares list little that a common max would have cut: no launch to reset it
+    if (!a.union_e && ((long long)a.B * a.nk * a.max_pages) << a.lc < 4ll * a.W) a.zmax = nullptr;
     if (a.zmax && !a.union_e) {
         e = launch_pdl(kv4_reset_kernel, dim3(ceil_div(heads, 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
-    if ((e = run_shares(kv4_scan_kernel<D, G>, a, st)) != cudaSuccess) return e;
+    if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
     const size_t smem = (size_t)(4 * TK_CAP + a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
@@ -1182,10 +1231,13 @@ cudaError_t decode_t(const Kv4DecodeArgs &a, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t decode_d(const Kv4DecodeArgs &a, cudaStream_t st) {
-    const int G = a.Hq / a.Hkv;
-    return G == 1 ? decode_t<D, 1>(a, st) : G == 2 ? decode_t<D, 2>(a, st) : G == 4 ? decode_t<D, 4>(a, st)
-                                                                                    : decode_t<D, 8>(a, st);
+cudaError_t decode_d(const Kv4DecodeArgs &a, int sms, cudaStream_t st) {
+    switch (a.Hq / a.Hkv) {
+        case 1: return decode_t<D, 1>(a, sms, st);
+        case 2: return decode_t<D, 2>(a, sms, st);
+        case 4: return decode_t<D, 4>(a, sms, st);
+        default: return decode_t<D, 8>(a, sms, st);
+    }
 }
 
 }  // namespace
@@ -1238,10 +1290,8 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.max_pages = s->max_pages;
     a.num_blocks = s->num_blocks;
     kv_range(s, &a.kv0, &a.nk);
-    a.lp = s->page_size == 16 ? 0 : s->page_size == 32 ? 1 : 2;
-    a.W = share_warps(s, a.nk, di.sms, alpha == 1.f ? 3 : 5);
-    // short shares list little that a common max would have cut: no launch to reset it
-    if (!sel && (long long)s->B * a.nk * s->max_pages << a.lp < 8ll * a.W) a.zmax = nullptr;
+    a.ct = s->page_size == 16 ? 1 : 2;
+    a.lc = s->page_size == 64 ? 1 : 0;
     a.alpha = alpha;
     a.r_int = alpha > 1.f ? integer_r(alpha) : 0;
     a.status = di.status;
@@ -1273,7 +1323,7 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
         a.union_blk = u.ws.union_blk;
         a.union_cnt = u.ws.union_cnt;
     }
-    const cudaError_t e = s->d == 64 ? decode_d<64>(a, st) : decode_d<128>(a, st);
+    const cudaError_t e = s->d == 64 ? decode_d<64>(a, di.sms, st) : decode_d<128>(a, di.sms, st);
     return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA;
 }
 
