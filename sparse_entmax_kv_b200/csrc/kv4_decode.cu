@@ -806,6 +806,9 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
     __shared__ int2 infos[AT_WARPS][RING_STAGES];
+    constexpr int EARLY = G == 8 ? 4 : 8;  // tiles a share begins with
+    __shared__ float early[AT_WARPS][EARLY * 16 * G];
+    __shared__ unsigned early_row[AT_WARPS][EARLY];
     __shared__ Plan<AT_THREADS> plan;
     plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -834,6 +837,77 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         float thr[2] = {-INFINITY, -INFINITY};    // below it a score carries no weight
         int n[G] = {};                            // candidates of each head
         bool bad[2] = {false, false};             // the lane saw a NaN score
+        int held = 0;                             // early tiles held back, -1 once they are settled
+
+        // lists the tokens of a tile that can still carry weight
+        auto test = [&](const float (&z)[4], unsigned row) {
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) any |= !(z[e] <= thr[e]) || !(z[2 + e] <= thr[e]);  // NaN stays a candidate
+            if (!__any_sync(FULL, any)) return;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
+                float tm = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
+                if (tm > m[e]) {
+                    m[e] = tm;
+                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
+                        atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
+                }
+                thr[e] = fmaxf(m[e], known[e]) - 1.f;
+            }
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                const int e = h & 1;
+                const bool mine = c == (h >> 1);
+                const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
+                const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
+                if (lo | hi) {
+                    const size_t at = list + h * row_len + n[h];
+                    const unsigned below = (1u << lane) - 1u;
+                    if ((lo >> lane) & 1u) {
+                        const size_t k = at + __popc(lo & below);
+                        a.cand_z[k] = z[e];
+                        a.cand_row[k] = row;
+                    }
+                    if ((hi >> lane) & 1u) {
+                        const size_t k = at + __popc(lo) + __popc(hi & below);
+                        a.cand_z[k] = z[2 + e];
+                        a.cand_row[k] = row + 8;
+                    }
+                    n[h] += __popc(lo) + __popc(hi);
+                }
+            }
+        };
+        // The first tiles of a share are tested together, against the largest
+        // score that the warps of the head have met in theirs (alone, a warp
+        // lists nearly all of them, and the tau kernel has to drop them again:
+        // entmax over 4 x 128k tokens 206 us without, see the table of times).
+        auto settle = [&] {
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
+                if (a.zmax) {
+                    if (r == 0 && 2 * c + e < G && m[e] > -INFINITY) atomicMax(a.zmax + h0 + 2 * c + e, f2ord(m[e]));
+                    known[e] = ord2f(__ldcg(a.zmax + h0 + (2 * c + e) % G));
+                }
+                thr[e] = fmaxf(m[e], known[e]) - 1.f;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < held; ++k) {
+                const float *from = early[warp] + k * 16 * G;
+                float z[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if ((v & 1) < NE) z[v] = from[(r + 8 * (v >> 1)) * G + (2 * c + (v & 1)) % G];
+                test(z, early_row[warp][k] + r);
+            }
+            held = -1;
+        };
         for (int i = sh.first; i < sh.last; ++i) {
             int2 what;
             unsigned char *stage;
@@ -846,7 +920,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                 for (int e = 0; e < NE; ++e) {
                     known[e] = fmaxf(known[e], ord2f(next[e]));
                     thr[e] = fmaxf(m[e], known[e]) - 1.f;
-                    if (2 * c + e < G) next[e] = __ldcg(a.zmax + h0 + 2 * c + e);
+                    next[e] = __ldcg(a.zmax + h0 + (2 * c + e) % G);
                 }
             }
             const int mask = what.y >> 8;
@@ -857,49 +931,23 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                 float z[4];
                 tile_scores<D, G>(tile, Q, z);
                 if (!whole<G>(mask, left)) mask_scores<G>(mask, left, z);
-                bool any = false;
-#pragma unroll
-                for (int e = 0; e < NE; ++e) any |= !(z[e] <= thr[e]) || !(z[2 + e] <= thr[e]);  // NaN stays a candidate
-                if (!__any_sync(FULL, any)) continue;
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
-                    float tm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
-                    if (tm > m[e]) {
-                        m[e] = tm;
-                        if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
-                            atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
-                    }
-                    thr[e] = fmaxf(m[e], known[e]) - 1.f;
+                if (held < 0) {
+                    test(z, row);
+                    continue;
                 }
+                float *to = early[warp] + held * 16 * G;
 #pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const int e = h & 1;
-                    const bool mine = c == (h >> 1);
-                    const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
-                    const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
-                    if (lo | hi) {
-                        const size_t at = list + h * row_len + n[h];
-                        const unsigned below = (1u << lane) - 1u;
-                        if ((lo >> lane) & 1u) {
-                            const size_t k = at + __popc(lo & below);
-                            a.cand_z[k] = z[e];
-                            a.cand_row[k] = row;
-                        }
-                        if ((hi >> lane) & 1u) {
-                            const size_t k = at + __popc(lo) + __popc(hi & below);
-                            a.cand_z[k] = z[2 + e];
-                            a.cand_row[k] = row + 8;
-                        }
-                        n[h] += __popc(lo) + __popc(hi);
-                    }
-                }
+                for (int v = 0; v < 4; ++v)
+                    if ((v & 1) < NE && 2 * c + (v & 1) < G) to[(r + 8 * (v >> 1)) * G + 2 * c + (v & 1)] = z[v];
+                if (r == 0) early_row[warp][held] = row;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) m[e] = fmaxf(m[e], fmaxf(z[e], z[2 + e]));
+                if (++held == EARLY) settle();
             }
             __syncwarp();
             if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
         }
+        if (held >= 0) settle();
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -913,7 +961,9 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
 
 constexpr int TK_NT = 256;
 constexpr int TK_NW = TK_NT / 32;
-constexpr int TK_CAP = 4096;  // candidates held on chip
+constexpr int TK_CAP = 4096;   // candidates held on chip
+constexpr int TK_EACH = 4;     // listed ones a thread takes at a time ...
+constexpr int TK_FLAT = 32768; // ... of lists up to this long in all; longer ones go a warp a share
 
 // One CTA a head: the candidates above the head's max - 1 in token order, their
 // threshold, and the sum of p v over the support.
@@ -924,14 +974,12 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     extern __shared__ int dyn[];
     float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates ...
     unsigned *crow = reinterpret_cast<unsigned *>(dyn + TK_CAP);    // [TK_CAP] ... and their value rows
-    float *raw_z = reinterpret_cast<float *>(dyn + 2 * TK_CAP);     // [TK_CAP] listed, before the cut
-    int *raw_at = dyn + 3 * TK_CAP;                                 // [TK_CAP]
-    int *seg_at = dyn + 4 * TK_CAP;                                 // [shares + 1] place of each share's candidates
+    int *seg_at = dyn + 2 * TK_CAP;                                 // [shares + 1] place of each share's candidates
     __shared__ Plan<TK_NT> plan;
     __shared__ float o_sh[TK_NW][D];
     __shared__ float red[2][TK_NW][2];
     __shared__ float s_max[TK_NW];
-    __shared__ int s_n[TK_NW];
+    __shared__ int s_n[TK_NW * TK_EACH + 1];
     __shared__ int scan[72];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.Hq / a.Hkv;
@@ -1014,52 +1062,63 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             }
         }
     };
-    if (R <= TK_CAP) {
-        // the lists as one range, a contiguous piece a warp
-        const int piece = ((R + TK_NT - 1) / TK_NT) * 32;
-        const int i1 = min(R, (warp + 1) * piece);
-        int kept = 0;
-        for (int i0 = warp * piece; i0 < i1; i0 += 32) {
-            const int i = i0 + lane;
-            bool keep = false;
-            if (i < i1) {
-                int lo = 0, hi = W - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (seg_at[mid] <= i) lo = mid;
-                    else hi = mid - 1;
-                }
-                const int at = seg_base(lo) + i - seg_at[lo];
-                const float z = __ldcg(zl + at);
-                raw_z[i] = z;
-                raw_at[i] = at;
-                keep = !(z <= thr);
-                bad |= z != z;
-            }
-            kept += __popc(__ballot_sync(FULL, keep));
-        }
-        if (lane == 0) s_n[warp] = kept;
-        __syncthreads();
-        int at = 0;
+    if (R <= TK_FLAT) {
+        // the lists as one range, TK_EACH places a thread at a time
         nc = 0;
+        for (int base = 0; base < R; base += TK_NT * TK_EACH) {
+            float z[TK_EACH];
+            int at[TK_EACH];
 #pragma unroll
-        for (int w = 0; w < TK_NW; ++w) {
-            if (w < warp) at += s_n[w];
-            nc += s_n[w];
-        }
-        for (int i0 = warp * piece; i0 < i1; i0 += 32) {
-            const int i = i0 + lane;
-            const float z = i < i1 ? raw_z[i] : -INFINITY;
-            const bool keep = !(z <= thr);
-            const unsigned bal = __ballot_sync(FULL, keep);
-            if (keep) {
-                const int k = at + __popc(bal & ((1u << lane) - 1u));
-                cz[k] = z;
-                crow[k] = __ldcg(rl + raw_at[i]);
+            for (int u = 0; u < TK_EACH; ++u) {
+                const int i = base + u * TK_NT + threadIdx.x;
+                z[u] = -INFINITY;
+                at[u] = 0;
+                if (i < R) {
+                    int lo = 0, hi = W - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (seg_at[mid] <= i) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    at[u] = seg_base(lo) + i - seg_at[lo];
+                    z[u] = __ldcg(zl + at[u]);
+                }
             }
-            at += __popc(bal);
+            unsigned keep[TK_EACH];
+#pragma unroll
+            for (int u = 0; u < TK_EACH; ++u) {
+                bad |= z[u] != z[u];
+                keep[u] = __ballot_sync(FULL, !(z[u] <= thr));
+                if (lane == 0) s_n[u * TK_NW + warp] = __popc(keep[u]);
+            }
+            __syncthreads();
+            if (threadIdx.x < 32) {
+                static_assert(TK_EACH * TK_NW == 32, "a warp scans the counts");
+                const int k = s_n[lane];
+                int x = k;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(FULL, x, o);
+                    if (lane >= o) x += y;
+                }
+                s_n[lane] = x - k;
+                if (lane == 31) s_n[32] = x;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < TK_EACH; ++u) {
+                const int k = nc + s_n[u * TK_NW + warp] + __popc(keep[u] & ((1u << lane) - 1u));
+                if (!(z[u] <= thr) && k < TK_CAP) {
+                    cz[k] = z[u];
+                    crow[k] = __ldcg(rl + at[u]);
+                }
+            }
+            nc += s_n[32];
+            __syncthreads();
         }
-    } else {
+        onchip = nc <= TK_CAP;
+    }
+    if (R > TK_FLAT || !onchip) {
         // how many of each share stay, and where they go
         for (int w = warp; w < W; w += TK_NW) {
             const int n = seg_size(w);
@@ -1224,7 +1283,7 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
-    const size_t smem = (size_t)(4 * TK_CAP + a.W + 1) * 4;
+    const size_t smem = (size_t)(2 * TK_CAP + a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
     return launch_pdl(k, dim3(heads), dim3(TK_NT), smem, st, a);

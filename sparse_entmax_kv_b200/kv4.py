@@ -54,6 +54,19 @@ def sized(t, shape, name):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def arg(t, dtype, shape, name, device, pinned_ok=False):
+    """Address of a contiguous tensor of this dtype and shape on the current device `device` (None stays None)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    p = nv._ptr(t, dtype, name, pinned_ok=pinned_ok)
+    sized(t, shape, name)
+    on_current_device(t)
+    return p
+
+
 def bytes_of(shape: nv.Shape) -> int:
     """Bytes of one 4-bit cache (keys or values)."""
     return lib().entmaxkv_kv4_bytes(C.byref(shape))
@@ -78,85 +91,81 @@ def alloc_workspace(shape: nv.Shape, device) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _cache_args(shape, k4, v4, page_table, seq_lens):
-    n = bytes_of(shape)
-    sized(k4, (n,), "k4")
-    sized(v4, (n,), "v4")
-    sized(page_table, (shape.B, shape.max_pages), "page_table")
-    sized(seq_lens, (shape.B,), "seq_lens")
-    on_current_device(k4, v4, page_table, seq_lens)
+def _cache_bytes(shape):
+    return shape.num_blocks * shape.Hkv * shape.page_size * shape.d // 16 * 9
+
+
+def _cache_args(shape, k4, v4, page_table, seq_lens, device):
+    n = (_cache_bytes(shape),)
+    return (arg(k4, torch.uint8, n, "k4", device), arg(v4, torch.uint8, n, "v4", device),
+            arg(page_table, torch.int32, (shape.B, shape.max_pages), "page_table", device),
+            arg(seq_lens, torch.int32, (shape.B,), "seq_lens", device))
 
 
 def _rows(shape, x, name, dtypes, pinned_ok):
-    """(pointer, row stride) of rows [n, Hkv, d] whose heads are packed; consecutive rows may lie apart."""
+    """(address, row stride) of rows [n, Hkv, d] whose heads are packed; consecutive rows may lie apart."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
     if not x.is_cuda and not (pinned_ok and x.device.type == "cpu" and x.is_pinned()):
         raise ValueError(f"{name}: must be a CUDA tensor" + (" or pinned" if pinned_ok else ""))
-    if x.dim() != 3 or x.shape[1] != shape.Hkv or x.shape[2] != shape.d:
-        raise ValueError(f"{name}: expected [rows, {shape.Hkv}, {shape.d}], got {tuple(x.shape)}")
-    if x.stride(2) != 1 or (shape.Hkv > 1 and x.stride(1) != shape.d):
+    Hkv, d = shape.Hkv, shape.d
+    n, row, form = x.shape[0] if x.dim() else 0, Hkv * d, x.stride()
+    if x.shape != (n, Hkv, d):
+        raise ValueError(f"{name}: expected [rows, {Hkv}, {d}], got {tuple(x.shape)}")
+    if form[2] != 1 or (Hkv > 1 and form[1] != d):
         raise ValueError(f"{name}: the heads of a row must be packed")
-    row = shape.Hkv * shape.d
-    return C.c_void_p(x.data_ptr()), x.stride(0) if x.shape[0] > 1 else row
+    return x.data_ptr(), form[0] if n > 1 else row
 
 
 def _row_pair(shape, k, v, names, dtypes, row_start, pinned_ok=False):
     pk, sk = _rows(shape, k, names[0], dtypes, pinned_ok)
     pv, sv = _rows(shape, v, names[1], dtypes, pinned_ok)
-    if k.shape[0] != v.shape[0] or sk != sv or k.dtype != v.dtype:
+    n = k.shape[0]
+    if n != v.shape[0] or sk != sv or k.dtype != v.dtype:
         raise ValueError(f"{names[0]} and {names[1]}: expected the same rows, strides and dtype")
-    if row_start is None:
-        if k.shape[0] != shape.B:
-            raise ValueError(f"{names[0]}: one row a sequence ({shape.B}) without row_start, got {k.shape[0]}")
-    else:
-        sized(row_start, (shape.B + 1,), "row_start")
-    on_current_device(k, v, row_start)
-    return pk, pv, sk, nv._ptr(row_start, torch.int32, "row_start")
+    device = torch.cuda.current_device()
+    for x in (k, v):
+        if x.is_cuda and x.get_device() != device:
+            on_current_device(x)
+    if row_start is None and n != shape.B:
+        raise ValueError(f"{names[0]}: one row a sequence ({shape.B}) without row_start, got {n}")
+    return pk, pv, sk, arg(row_start, torch.int32, (shape.B + 1,), "row_start", device), n, device
 
 
 def entmaxkv_kv4_write(shape, k_new, v_new, row_start, page_table, seq_lens, k4, v4, meta=None, stream=None):
     """Rows bf16 [n, Hkv, d] (row b of every sequence b when row_start is None) into the cache, as the last tokens of
     their sequences; with meta, the records of the pages they touch.  Rows may be pinned host tensors."""
-    pk, pv, stride, ps = _row_pair(shape, k_new, v_new, ("k_new", "v_new"), (torch.bfloat16,), row_start, True)
-    _cache_args(shape, k4, v4, page_table, seq_lens)
-    if meta is not None:
-        sized(meta, (nv.meta_bytes(shape),), "meta")
-        on_current_device(meta)
+    pk, pv, stride, ps, n, device = _row_pair(shape, k_new, v_new, ("k_new", "v_new"), (torch.bfloat16,), row_start,
+                                              True)
+    c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
+    m = None if meta is None else arg(meta, torch.uint8, (nv.meta_bytes(shape),), "meta", device)
     nv._check("entmaxkv_kv4_write", lib().entmaxkv_kv4_write(
-        C.byref(shape), pk, pv, stride, ps, k_new.shape[0], nv._ptr(page_table, torch.int32, "page_table"),
-        nv._ptr(seq_lens, torch.int32, "seq_lens"), nv._ptr(k4, torch.uint8, "k4"), nv._ptr(v4, torch.uint8, "v4"),
-        nv._ptr(meta, torch.uint8, "meta"), nv._stream(stream)))
+        C.byref(shape), pk, pv, stride, ps, n, pt, sl, c4k, c4v, m, nv._stream(stream)))
 
 
 def entmaxkv_kv4_read(shape, k4, v4, row_start, page_table, seq_lens, k_out, v_out, stream=None):
     """The last tokens of every sequence into rows [n, Hkv, d], bf16 or fp32: the inverse of entmaxkv_kv4_write."""
-    pk, pv, stride, ps = _row_pair(shape, k_out, v_out, ("k_out", "v_out"), tuple(_ROWS), row_start)
-    _cache_args(shape, k4, v4, page_table, seq_lens)
+    pk, pv, stride, ps, n, device = _row_pair(shape, k_out, v_out, ("k_out", "v_out"), tuple(_ROWS), row_start)
+    c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
     nv._check("entmaxkv_kv4_read", lib().entmaxkv_kv4_read(
-        C.byref(shape), nv._ptr(k4, torch.uint8, "k4"), nv._ptr(v4, torch.uint8, "v4"), stride, ps, k_out.shape[0],
-        nv._ptr(page_table, torch.int32, "page_table"), nv._ptr(seq_lens, torch.int32, "seq_lens"),
-        _ROWS[k_out.dtype], pk, pv, nv._stream(stream)))
+        C.byref(shape), c4k, c4v, stride, ps, n, pt, sl, _ROWS[k_out.dtype], pk, pv, nv._stream(stream)))
 
 
 def entmaxkv_kv4_decode(shape, q, k4, v4, page_table, seq_lens, alpha, out, tau_out=None, sel=None, cnt=None, *,
                         workspace, stream=None):
     """Attention of q (bf16 [B, Hq, d]) over the 4-bit cache into out (fp32 [B, Hq, d]): softmax (alpha = 1) or
     alpha-entmax, over the selected pages, or over all of them without sel and cnt."""
+    device = torch.cuda.current_device()
     heads = (shape.B, shape.Hq)
-    _cache_args(shape, k4, v4, page_table, seq_lens)
-    sized(q, heads + (shape.d,), "q")
-    sized(out, heads + (shape.d,), "out")
-    sized(tau_out, heads, "tau_out")
-    sized(sel, heads + (shape.max_pages,), "sel")
-    sized(cnt, heads, "cnt")
-    on_current_device(q, out, tau_out, sel, cnt, workspace)
+    rows = heads + (shape.d,)
+    c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
+    ws = nv._ptr(workspace, torch.uint8, "workspace")
+    if workspace.get_device() != device:
+        on_current_device(workspace)
     nv._check("entmaxkv_kv4_decode", lib().entmaxkv_kv4_decode(
-        C.byref(shape), nv._ptr(q, torch.bfloat16, "q"), nv._ptr(k4, torch.uint8, "k4"),
-        nv._ptr(v4, torch.uint8, "v4"), nv._ptr(page_table, torch.int32, "page_table"),
-        nv._ptr(seq_lens, torch.int32, "seq_lens"), nv._ptr(sel, torch.int32, "sel"),
-        nv._ptr(cnt, torch.int32, "cnt"), float(alpha), nv._ptr(out, torch.float32, "out", pinned_ok=True),
-        nv._ptr(tau_out, torch.float32, "tau_out"), nv._ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-        nv._stream(stream)))
+        C.byref(shape), arg(q, torch.bfloat16, rows, "q", device), c4k, c4v, pt, sl,
+        arg(sel, torch.int32, heads + (shape.max_pages,), "sel", device), arg(cnt, torch.int32, heads, "cnt", device),
+        float(alpha), arg(out, torch.float32, rows, "out", device, pinned_ok=True),
+        arg(tau_out, torch.float32, heads, "tau_out", device), ws, workspace.numel(), nv._stream(stream)))

@@ -12,7 +12,7 @@ import ctypes as C
 import torch
 
 from . import native as nv
-from .kv4 import on_current_device, sized
+from .kv4 import arg, on_current_device
 
 EXPORTED = ("entmaxkv_pages_workspace_size", "entmaxkv_pages_refs", "entmaxkv_pages_fork", "entmaxkv_pages_grow",
             "entmaxkv_pages_compact", "entmaxkv_pages_copy")
@@ -49,6 +49,13 @@ class Buffers:
             raise ValueError(f"buffers: {size} bytes are not {self.num_blocks} equal blocks")
         self.base = (C.c_void_p * max(1, len(self.tensors)))(*[t.data_ptr() for t in self.tensors])
         self.c = _CBuffers(len(self.tensors), size // self.num_blocks if self.tensors else 0, self.base)
+        self.ref = C.byref(self.c)
+        self.device = self.tensors[0].get_device() if self.tensors else -1  # -1: host memory
+
+    def on(self, device):
+        """The buffers have to live on the current device `device`, or in host memory."""
+        if self.device >= 0 and self.device != device:
+            on_current_device(self.tensors[0])
 
 
 _ready = None
@@ -81,91 +88,91 @@ def alloc_workspace(shape: nv.Shape, device) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _i32(t, shape, name):
-    if t is None:
-        return None
-    sized(t, shape, name)
-    on_current_device(t)
-    return nv._ptr(t, torch.int32, name)
+def _i32(t, shape, name, device):
+    return arg(t, torch.int32, shape, name, device)
 
 
-def _buffers(b, shape, name):
+def _buffers(b, shape, name, device):
     if b is None:
         return None
     if not isinstance(b, Buffers):
         raise TypeError(f"{name}: expected pages.Buffers")
     if b.tensors and b.num_blocks != shape.num_blocks:
         raise ValueError(f"{name}: {b.num_blocks} blocks, the shape has {shape.num_blocks}")
-    on_current_device(*b.tensors[:1])
-    return C.byref(b.c)
+    b.on(device)
+    return b.ref
 
 
-def _metas(b, shape, name):
+def _metas(b, shape, name, device):
     if b is None:
         return None
     if not isinstance(b, Buffers):
         raise TypeError(f"{name}: expected pages.Buffers")
     if b.tensors and b.nbytes != nv.meta_bytes(shape):
         raise ValueError(f"{name}: metadata buffers of {nv.meta_bytes(shape)} bytes expected, got {b.nbytes}")
-    on_current_device(*b.tensors[:1])
-    return C.byref(b.c)
+    b.on(device)
+    return b.ref
 
 
-def _ws(workspace):
-    on_current_device(workspace)
-    return nv._ptr(workspace, torch.uint8, "workspace"), workspace.numel()
+def _ws(workspace, device):
+    p = nv._ptr(workspace, torch.uint8, "workspace")
+    if workspace.get_device() != device:
+        on_current_device(workspace)
+    return p, workspace.numel()
 
 
 def entmaxkv_pages_refs(shape, page_table, seq_lens, refs=None, n_free=None, hold=None, *, workspace, stream=None):
     """refs (int32 [num_blocks]): rows that reach each block, plus holds; n_free (int32 [1]): blocks without any."""
-    nb = shape.num_blocks
+    B, nb, dev = shape.B, shape.num_blocks, torch.cuda.current_device()
     nv._check("entmaxkv_pages_refs", lib().entmaxkv_pages_refs(
-        C.byref(shape), _i32(page_table, (shape.B, shape.max_pages), "page_table"), _i32(seq_lens, (shape.B,), "seq_lens"),
-        _i32(hold, (nb,), "hold"), _i32(refs, (nb,), "refs"), _i32(n_free, (1,), "n_free"), *_ws(workspace),
-        nv._stream(stream)))
+        C.byref(shape), _i32(page_table, (B, shape.max_pages), "page_table", dev),
+        _i32(seq_lens, (B,), "seq_lens", dev), _i32(hold, (nb,), "hold", dev), _i32(refs, (nb,), "refs", dev),
+        _i32(n_free, (1,), "n_free", dev), *_ws(workspace, dev), nv._stream(stream)))
 
 
 def entmaxkv_pages_fork(shape, parent, table_in, lens_in, table_out, lens_out, buffers, meta_in=None, meta_out=None,
                         hold=None, *, workspace, stream=None):
     """Row b of the new table continues row parent[b] of the old one (-1: empty); full pages are shared, partial last
     pages copied in every buffer; metadata buffers follow their rows.  In place when the out tensors are the in ones."""
-    B, table = shape.B, (shape.B, shape.max_pages)
+    B, table, dev = shape.B, (shape.B, shape.max_pages), torch.cuda.current_device()
     nv._check("entmaxkv_pages_fork", lib().entmaxkv_pages_fork(
-        C.byref(shape), _i32(parent, (B,), "parent"), _i32(table_in, table, "table_in"), _i32(lens_in, (B,), "lens_in"),
-        _i32(hold, (shape.num_blocks,), "hold"), _i32(table_out, table, "table_out"), _i32(lens_out, (B,), "lens_out"),
-        _buffers(buffers, shape, "buffers"), _metas(meta_in, shape, "meta_in"), _metas(meta_out, shape, "meta_out"),
-        *_ws(workspace), nv._stream(stream)))
+        C.byref(shape), _i32(parent, (B,), "parent", dev), _i32(table_in, table, "table_in", dev),
+        _i32(lens_in, (B,), "lens_in", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
+        _i32(table_out, table, "table_out", dev), _i32(lens_out, (B,), "lens_out", dev),
+        _buffers(buffers, shape, "buffers", dev), _metas(meta_in, shape, "meta_in", dev),
+        _metas(meta_out, shape, "meta_out", dev), *_ws(workspace, dev), nv._stream(stream)))
 
 
 def entmaxkv_pages_grow(shape, n_add, page_table, seq_lens, hold=None, *, workspace, stream=None):
     """Sequence b grows by n_add[b] tokens, in place: new pages get the lowest free blocks."""
-    B = shape.B
+    B, dev = shape.B, torch.cuda.current_device()
     nv._check("entmaxkv_pages_grow", lib().entmaxkv_pages_grow(
-        C.byref(shape), _i32(n_add, (B,), "n_add"), _i32(hold, (shape.num_blocks,), "hold"),
-        _i32(page_table, (B, shape.max_pages), "page_table"), _i32(seq_lens, (B,), "seq_lens"), *_ws(workspace),
-        nv._stream(stream)))
+        C.byref(shape), _i32(n_add, (B,), "n_add", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
+        _i32(page_table, (B, shape.max_pages), "page_table", dev), _i32(seq_lens, (B,), "seq_lens", dev),
+        *_ws(workspace, dev), nv._stream(stream)))
 
 
 def entmaxkv_pages_compact(shape, table_in, seq_lens, table_out, buffers, remap, n_live, hold=None, *, workspace,
                            stream=None):
     """Used blocks move below n_live, their count; the table follows (table_out may be table_in)."""
-    table = (shape.B, shape.max_pages)
+    table, nb, dev = (shape.B, shape.max_pages), (shape.num_blocks,), torch.cuda.current_device()
     nv._check("entmaxkv_pages_compact", lib().entmaxkv_pages_compact(
-        C.byref(shape), _i32(table_in, table, "table_in"), _i32(seq_lens, (shape.B,), "seq_lens"),
-        _i32(hold, (shape.num_blocks,), "hold"), _i32(table_out, table, "table_out"),
-        _buffers(buffers, shape, "buffers"), _i32(remap, (shape.num_blocks,), "remap"), _i32(n_live, (1,), "n_live"),
-        *_ws(workspace), nv._stream(stream)))
+        C.byref(shape), _i32(table_in, table, "table_in", dev), _i32(seq_lens, (shape.B,), "seq_lens", dev),
+        _i32(hold, nb, "hold", dev), _i32(table_out, table, "table_out", dev), _buffers(buffers, shape, "buffers", dev),
+        _i32(remap, nb, "remap", dev), _i32(n_live, (1,), "n_live", dev), *_ws(workspace, dev), nv._stream(stream)))
 
 
 def entmaxkv_pages_copy(src, dst, src_ids, dst_ids, stream=None):
     """Block dst_ids[i] of every dst buffer := block src_ids[i] of the src buffer of the same number.  Either side
     may be pinned host memory."""
+    dev = torch.cuda.current_device()
     for b, name in ((src, "src"), (dst, "dst")):
         if not isinstance(b, Buffers):
             raise TypeError(f"{name}: expected pages.Buffers")
-        on_current_device(*b.tensors[:1])
-    if src_ids.dim() != 1:
+        b.on(dev)
+    if not isinstance(src_ids, torch.Tensor) or src_ids.dim() != 1:
         raise ValueError("src_ids: expected one dimension")
+    ids = (src_ids.shape[0],)
     nv._check("entmaxkv_pages_copy", lib().entmaxkv_pages_copy(
-        C.byref(src.c), src.num_blocks, C.byref(dst.c), dst.num_blocks, _i32(src_ids, src_ids.shape, "src_ids"),
-        _i32(dst_ids, src_ids.shape, "dst_ids"), src_ids.numel(), nv._stream(stream)))
+        src.ref, src.num_blocks, dst.ref, dst.num_blocks, _i32(src_ids, ids, "src_ids", dev),
+        _i32(dst_ids, ids, "dst_ids", dev), ids[0], nv._stream(stream)))
