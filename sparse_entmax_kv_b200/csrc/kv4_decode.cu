@@ -816,6 +816,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     if (w >= plan.warps(a)) return;
     Ring ring;
     ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
+    const unsigned column = 0x11111111u << c, below = (1u << lane) - 1u;  // lanes of the same columns
     const size_t row_len = (size_t)a.max_pages * a.P;
     long long t = plan.first_of(a, w);
     const long long end = plan.first_of(a, w + 1);
@@ -829,17 +830,19 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         const int h0 = sh.b * a.Hq + sh.kvh * G;
         Queries<D, G> Q;
         Q.load(a.q + (size_t)h0 * D, (a.alpha - 1.f) * rsqrtf((float)D));
-        const size_t list = (size_t)h0 * row_len + (size_t)sh.first * (16 * a.ct);
+        const size_t list = (size_t)(h0 + 2 * c) * row_len + (size_t)sh.first * (16 * a.ct);
 
-        float m[2] = {-INFINITY, -INFINITY};      // the share's max so far, of the lane's columns
+        float m[2] = {-INFINITY, -INFINITY};      // the lane's max so far, of its columns
         float known[2] = {-INFINITY, -INFINITY};  // what other shares of the head have reported
         int next[2] = {ORD_NEG_INF, ORD_NEG_INF};
         float thr[2] = {-INFINITY, -INFINITY};    // below it a score carries no weight
-        int n[G] = {};                            // candidates of each head
+        int n[2] = {0, 0};                        // candidates of the lane's columns
         bool bad[2] = {false, false};             // the lane saw a NaN score
         int held = 0;                             // early tiles held back, -1 once they are settled
 
-        // lists the tokens of a tile that can still carry weight
+        // Lists the tokens of a tile that can still carry weight.  A lane goes
+        // by the largest score it knows of; a new one reaches the other lanes
+        // through the head's shared max.
         auto test = [&](const float (&z)[4], unsigned row) {
             bool any = false;
 #pragma unroll
@@ -848,25 +851,16 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
                 bad[e] |= z[e] != z[e] || z[2 + e] != z[2 + e];
-                float tm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, o));
+                const float tm = fmaxf(z[e], z[2 + e]);
                 if (tm > m[e]) {
                     m[e] = tm;
-                    if (a.zmax && tm > known[e] && r == 0 && 2 * c + e < G)
-                        atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
+                    if (a.zmax && tm > known[e] && 2 * c + e < G) atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
+                    thr[e] = fmaxf(thr[e], tm - 1.f);
                 }
-                thr[e] = fmaxf(m[e], known[e]) - 1.f;
-            }
-#pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const int e = h & 1;
-                const bool mine = c == (h >> 1);
-                const unsigned lo = __ballot_sync(FULL, mine && !(z[e] <= thr[e]));
-                const unsigned hi = __ballot_sync(FULL, mine && !(z[2 + e] <= thr[e]));
-                if (lo | hi) {
-                    const size_t at = list + h * row_len + n[h];
-                    const unsigned below = (1u << lane) - 1u;
+                const unsigned lo = __ballot_sync(FULL, !(z[e] <= thr[e])) & column;
+                const unsigned hi = __ballot_sync(FULL, !(z[2 + e] <= thr[e])) & column;
+                if (2 * c + e < G) {
+                    const size_t at = list + e * row_len + n[e];
                     if ((lo >> lane) & 1u) {
                         const size_t k = at + __popc(lo & below);
                         a.cand_z[k] = z[e];
@@ -877,8 +871,8 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                         a.cand_z[k] = z[2 + e];
                         a.cand_row[k] = row + 8;
                     }
-                    n[h] += __popc(lo) + __popc(hi);
                 }
+                n[e] += __popc(lo) + __popc(hi);
             }
         };
         // The first tiles of a share are tested together, against the largest
@@ -915,7 +909,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                 ring.drain(a);
                 return;
             }
-            if (a.zmax && (i & 1)) {  // used two chunks on: nothing waits for the load
+            if (a.zmax && (i & 3) == 3) {  // used four chunks on: nothing waits for the load
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     known[e] = fmaxf(known[e], ord2f(next[e]));
@@ -950,11 +944,12 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         if (held >= 0) settle();
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-            float mh = __shfl_sync(FULL, m[h & 1], h >> 1);
+        for (int e = 0; e < NE; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
             // a NaN stays a candidate: its share may not be passed over for a low max
-            if (__any_sync(FULL, c == (h >> 1) && bad[h & 1])) mh = __int_as_float(0x7fc00000);
-            if (lane == 0) a.seg[slot * G + h] = make_int2(n[h], __float_as_int(mh));
+            if (__ballot_sync(FULL, bad[e]) & column) m[e] = __int_as_float(0x7fc00000);
+            if (r == 0 && 2 * c + e < G) a.seg[slot * G + 2 * c + e] = make_int2(n[e], __float_as_int(m[e]));
         }
     }
 }
