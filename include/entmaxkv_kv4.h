@@ -62,7 +62,8 @@ ENTMAXKV_API size_t entmaxkv_kv4_bytes(const entmaxkv_shape *shape);
  * from the values its codes stand for, in the layout of entmaxkv_meta_bytes:
  * kmin rounded down and kmax up to bf16, so that the page bound of
  * entmaxkv_score_pages bounds the scores of the 4-bit keys; mean and var as
- * in entmaxkv_build_meta (sums in fp64, token order).
+ * in entmaxkv_build_meta (sums in fp64: partial sums of every 1024/d-th token,
+ * added in order).
  * Sequences with n_b = 0 or a length <= 0 are skipped.  A sequence with
  * n_b < 0, n_b > seq_lens[b], rows outside [0, n_rows) or a length above
  * max_pages * P is skipped and sets ENTMAXKV_STATUS_BAD_LENGTH; a page with a

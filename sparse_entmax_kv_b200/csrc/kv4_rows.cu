@@ -1,14 +1,16 @@
 // kv4_rows.cu -- rows into and out of the 4-bit cache, and the C entry points
 // of both (include/entmaxkv_kv4.h).
 //
-// write: one CTA per (touched page, kv head).  A warp takes a token pair: its
-// lanes hold 4 (d = 128) or 2 (d = 64) neighbouring coordinates of both rows,
-// min and max of a 64-coordinate group come from shuffles, and the codes of a
-// word are joined across the lanes that share it.  A value word holds both
-// tokens of a pair; when only one of them is new the other's half is kept
-// (the warp is the word's only writer).  With metadata the page's dequantised
-// keys are kept in shared memory and thread j then walks coordinate j in
-// token order, as the bf16 build does.
+// write: one CTA per (touched page, kv head).  A lane takes 16 neighbouring
+// coordinates of a key row and of the value row of the same token, so that a
+// 64-coordinate group is four lanes: min and max are packed bf16 operations in
+// a lane and two shuffles, and a code costs five instructions (the rounding to
+// an integer is an addition of 1.5 2^23, whose low bits are then shifted into
+// place by an integer multiply-add).  A value word holds both tokens of a
+// pair: the two lanes trade halves, and where only one token is new the other
+// half of the word is kept (the lane is the word's only writer).  With
+// metadata the page's key tiles are also kept in shared memory, old tokens
+// copied in, and 1024 / d threads share the statistics of a coordinate.
 // read: the same split, the other way round.
 #include <cmath>
 
@@ -19,8 +21,9 @@ namespace ekv {
 
 namespace {
 
-constexpr int RW_THREADS = 128;
+constexpr int RW_THREADS = 256;
 constexpr int RW_WARPS = RW_THREADS / 32;
+constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, ties to even
 
 // What one CTA works on: tokens [t0, t1) of logical page `page` of sequence
 // b are new, [0, n) hold valid tokens, row0 is the row of token t0.
@@ -39,11 +42,14 @@ __device__ __forceinline__ bool page_job(const Kv4RowArgs &a, int slot, PageJob 
         if (slot == 0 && blockIdx.y == 0)  // rows that run backwards may own no slot: the first CTA looks at them all
             for (int i = threadIdx.x; i < a.m.B; i += blockDim.x)
                 if (a.row_start[i + 1] < a.row_start[i]) atomicOr(a.m.status, ENTMAXKV_STATUS_BAD_LENGTH);
-        int lo = 0, hi = a.m.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.row_start[mid] / P + 2 * mid <= slot) lo = mid;
-            else hi = mid - 1;
+        // the last sequence whose slots begin at or before this one, 32 tries at a time
+        int lo = 0;
+        for (int n = a.m.B; n > 1;) {
+            const int step = (n + 31) / 32, at = (int)(threadIdx.x & 31) * step;
+            const unsigned before = __ballot_sync(FULL, at < n && a.row_start[lo + at] / P + 2 * (lo + at) <= slot);
+            const int k = max(0, __popc(before) - 1) * step;
+            lo += k;
+            n = min(step, n - k);
         }
         b = lo;
         first = a.row_start[b];
@@ -80,141 +86,83 @@ __device__ __forceinline__ bool page_job(const Kv4RowArgs &a, int slot, PageJob 
     return true;
 }
 
+// Lanes of a row, and the rows that a warp takes at a time.
 template <int D>
-constexpr int CPL = D / 32;  // coordinates of a lane
+constexpr int LPR = D / 16;
+template <int D>
+constexpr int RPW = 32 / LPR<D>;
 
-// The lane's coordinates of a bf16 row.
-template <int D>
-__device__ __forceinline__ void load_row(const uint16_t *row, float (&x)[CPL<D>]) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(row + 4 * lane);
-        x[0] = bf16lo(w.x);
-        x[1] = bf16hi(w.x);
-        x[2] = bf16lo(w.y);
-        x[3] = bf16hi(w.y);
-    } else {
-        const unsigned w = *reinterpret_cast<const unsigned *>(row + 2 * lane);
-        x[0] = bf16lo(w);
-        x[1] = bf16hi(w);
-    }
+__device__ __forceinline__ unsigned min2(unsigned x, unsigned y) {
+    unsigned r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ unsigned max2(unsigned x, unsigned y) {
+    unsigned r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
 }
 
-// Codes of one row's coordinates held by the warp, and its group's parameters
-// (every lane of the group returns them).
-template <int D>
-__device__ __forceinline__ void quantise(const float (&x)[CPL<D>], unsigned (&c)[CPL<D>], float &s, float &lo) {
-    float mn = x[0], mx = x[0];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < CPL<D>; ++i) {
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-        bad |= !(fabsf(x[i]) < INFINITY);
+struct Row16 {
+    unsigned x[8];  // 16 bf16, then their codes' bits
+    __device__ __forceinline__ void load(const uint16_t *row) {
+        const uint4 a = reinterpret_cast<const uint4 *>(row)[0], b = reinterpret_cast<const uint4 *>(row)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int o = D == 128 ? 8 : 16; o; o >>= 1) {
-        mn = fminf(mn, __shfl_xor_sync(FULL, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        for (int i = 0; i < 8; ++i) x[i] = 0u;
     }
-    const unsigned bal = __ballot_sync(FULL, bad);
-    const int lane = threadIdx.x & 31;
-    const unsigned mine = D == 128 ? (lane < 16 ? 0xffffu : 0xffff0000u) : FULL;
-    const float range = __fsub_rn(mx, mn);
-    if ((bal & mine) || !(range < INFINITY)) {
-        s = lo = __int_as_float(0x7fc00000);
+};
+
+// Codes of the 16 coordinates as c + constants in two words of eight (KEYS:
+// coordinate n of a word at bits 16 (n & 1) + 4 (n >> 1); else in two words of
+// two quads each, coordinate n of a quad at bits 4 n), and the parameter word
+// of the group, which its four lanes return alike.
+template <bool KEYS>
+__device__ __forceinline__ unsigned quantise(const Row16 &row, unsigned (&w)[2]) {
+    unsigned mn = row.x[0], mx = row.x[0];
 #pragma unroll
-        for (int i = 0; i < CPL<D>; ++i) c[i] = 0u;
-        return;
+    for (int i = 1; i < 8; ++i) {
+        mn = min2(mn, row.x[i]);
+        mx = max2(mx, row.x[i]);
     }
-    lo = mn;
-    s = bf16f(f2bf(__fdiv_rn(range, 15.f)));
+    // the smallest in the low half, the largest in the high one
+    unsigned m = __byte_perm(min2(mn, mn >> 16), max2(mx, mx << 16), 0x7610);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        const unsigned y = __shfl_xor_sync(FULL, m, o);
+        m = __byte_perm(min2(m, y), max2(m, y), 0x7610);
+    }
+    const float lo = bf16lo(m);
+    const float range = __fsub_rn(bf16hi(m), lo);
+    if (!(range < INFINITY)) {  // a NaN (it stays through min and max), an infinity, or an overflow
+        w[0] = w[1] = 0u;
+        return 0x7fc07fc0u;
+    }
+    float s = bf16f(f2bf(__fdiv_rn(range, 15.f)));
     if (s < 1.17549435e-38f) s = 0.f;  // 2^-126: below, 1 / s may overflow
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    // s is within 2^-9 of range / 15, so no quotient exceeds 15.04: no clamp
 #pragma unroll
-    for (int i = 0; i < CPL<D>; ++i)
-        c[i] = (unsigned)fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], lo), inv)), 0.f), 15.f);
-}
-
-// Joins the lane's codes of a key row into its 8-coordinate word (all lanes
-// that share the word return it).
-template <int D>
-__device__ __forceinline__ unsigned join_k(const unsigned (&c)[CPL<D>]) {
-    const int lane = threadIdx.x & 31;
-    unsigned w;
-    if constexpr (D == 128) {
-        w = (c[0] | (c[1] << 16) | (c[2] << 4) | (c[3] << 20)) << (8 * (lane & 1));
-    } else {
-        w = (c[0] | (c[1] << 16)) << (4 * (lane & 3));
-        w |= __shfl_xor_sync(FULL, w, 2);
-    }
-    return w | __shfl_xor_sync(FULL, w, 1);
-}
-// The 16 bits of a value row's 4-coordinate word.
-template <int D>
-__device__ __forceinline__ unsigned join_v(const unsigned (&c)[CPL<D>]) {
-    if constexpr (D == 128) {
-        return c[0] | (c[1] << 4) | (c[2] << 8) | (c[3] << 12);
-    } else {
-        const unsigned w = (c[0] | (c[1] << 4)) << (8 * (threadIdx.x & 1));
-        return w | __shfl_xor_sync(FULL, w, 1);
-    }
-}
-// The lane's codes of token t's key / value from its stored words.
-template <int D>
-__device__ __forceinline__ void split_k(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (D == 128) {
-        const unsigned w = tile[kv4_kword<D>(t, lane >> 1)] >> (8 * (lane & 1));
-        c[0] = w & 15;
-        c[1] = (w >> 16) & 15;
-        c[2] = (w >> 4) & 15;
-        c[3] = (w >> 20) & 15;
-    } else {
-        const unsigned w = tile[kv4_kword<D>(t, lane >> 2)] >> (4 * (lane & 3));
-        c[0] = w & 15;
-        c[1] = (w >> 16) & 15;
-    }
-}
-template <int D>
-__device__ __forceinline__ void split_v(const unsigned *tile, int t, unsigned (&c)[CPL<D>]) {
-    const int lane = threadIdx.x & 31;
-    const int q4 = D == 128 ? lane : lane >> 1;
-    unsigned w = tile[kv4_vword<D>(t >> 1, q4)] >> (16 * (t & 1));
-    if constexpr (D == 64) w >>= 8 * (lane & 1);
+    for (int i = 0; i < 2; ++i) {
+        w[i] = 0u;
+        unsigned bias = 0u;  // what ROUND's bits add up to
 #pragma unroll
-    for (int i = 0; i < CPL<D>; ++i) c[i] = (w >> (4 * i)) & 15;
-}
-
-__device__ __forceinline__ unsigned pack_params(float s, float lo) {
-    return (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);  // both are bf16 values
-}
-
-// Group of the lane's coordinates.
-template <int D>
-__device__ __forceinline__ int lane_group() {
-    return D == 128 ? (int)(threadIdx.x & 31) >> 4 : 0;
-}
-// One lane of each group writes the group's parameters.
-template <int D>
-__device__ __forceinline__ bool group_leader() {
-    return (threadIdx.x & (D == 128 ? 15 : 31)) == 0;
-}
-
-template <int D>
-__device__ __forceinline__ void write_key(unsigned char *tile, int t, const float (&x)[CPL<D>], float *kval) {
-    unsigned c[CPL<D>];
-    float s, lo;
-    quantise<D>(x, c, s, lo);
-    const unsigned w = join_k<D>(c);
-    const int lane = threadIdx.x & 31;
-    constexpr int SH = D == 128 ? 2 : 4;  // lanes of a word
-    if (lane % SH == 0) reinterpret_cast<unsigned *>(tile)[kv4_kword<D>(t, lane / SH)] = w;
-    if (group_leader<D>())
-        reinterpret_cast<unsigned *>(tile + Kv4<D>::CODES)[t * Kv4<D>::NG + lane_group<D>()] = pack_params(s, lo);
-    if (kval)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < CPL<D>; ++i) kval[CPL<D> * lane + i] = __fmaf_rn(s, (float)c[i], lo);
+            for (int h = 0; h < 2; ++h) {
+                const unsigned xx = row.x[4 * i + k];
+                const float x = h ? bf16hi(xx) : bf16lo(xx);
+                const unsigned c = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x, lo), inv), ROUND));
+                const unsigned place = KEYS ? 1u << (16 * h + 4 * k) : 1u << (8 * k + 4 * h);
+                w[i] += c * place;
+                bias += 0x4b400000u * place;
+            }
+        w[i] -= bias;
+    }
+    return (__float_as_uint(s) >> 16) | (m << 16);
 }
 
 // bf16 neighbours of x on either side (x itself when it is a bf16 value).
@@ -229,10 +177,102 @@ __device__ __forceinline__ uint16_t bf16_up(float x) {
     return (uint16_t)((x > 0.f ? u + 0xffffu : u) >> 16);
 }
 
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+// A code (the low 4 bits) as a float: 2^23 + c, less 2^23.
+__device__ __forceinline__ float code_f32(unsigned c) { return __uint_as_float((c & 15u) | 0x4b000000u) - 8388608.f; }
+
+// The metadata record of a page from its key tiles in shared memory.  A thread
+// takes four coordinates (half a word, one pair of parameters a token), so
+// 1024 / d threads share them, each every (1024 / d)-th token; their sums are
+// added in order.
+template <int D>
+struct Stats {
+    static constexpr int PARTS = 4 * RW_THREADS / D;
+    double s1[PARTS][D], s2[PARTS][D];
+    float mn[PARTS][D], mx[PARTS][D];
+};
+template <int D>
+__device__ __forceinline__ void build_record(const MetaArgs &m, const unsigned char *image, Stats<D> &sh, int b, int kvh,
+                                             int page, int n) {
+    constexpr int PARTS = Stats<D>::PARTS;
+    {
+        const int q = threadIdx.x % (D / 4), part = threadIdx.x / (D / 4);
+        const unsigned *words = reinterpret_cast<const unsigned *>(image);
+        const int at = kv4_kword<D>(0, q >> 1), pat = Kv4<D>::CODES / 4 + (q >> 4), shift = 8 * (q & 1);
+        float mn[4], mx[4];
+        double s1[4], s2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mn[i] = INFINITY;
+            mx[i] = -INFINITY;
+            s1[i] = s2[i] = 0.0;
+        }
+#pragma unroll 2
+        for (int t = part; t < n; t += PARTS) {
+            const unsigned *tile = words + (t >> 4) * (Kv4<D>::TILE / 4);
+            const unsigned w = tile[at + (t & 15) * (D / 8)] >> shift, pr = tile[pat + (t & 15) * Kv4<D>::NG];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __fmaf_rn(bf16lo(pr), code_f32(w >> (16 * (i & 1) + 4 * (i >> 1))), bf16hi(pr));
+                mn[i] = min_nan(mn[i], x);
+                mx[i] = max_nan(mx[i], x);
+                const double xd = (double)x;
+                s1[i] = __dadd_rn(s1[i], xd);
+                s2[i] = __fma_rn(xd, xd, s2[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sh.s1[part][4 * q + i] = s1[i];
+            sh.s2[part][4 * q + i] = s2[i];
+            sh.mn[part][4 * q + i] = mn[i];
+            sh.mx[part][4 * q + i] = mx[i];
+        }
+    }
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j >= D) return;
+    double s1 = sh.s1[0][j], s2 = sh.s2[0][j];
+    float mn = sh.mn[0][j], mx = sh.mx[0][j];
+#pragma unroll
+    for (int k = 1; k < PARTS; ++k) {
+        s1 = __dadd_rn(s1, sh.s1[k][j]);
+        s2 = __dadd_rn(s2, sh.s2[k][j]);
+        mn = min_nan(mn, sh.mn[k][j]);
+        mx = max_nan(mx, sh.mx[k][j]);
+    }
+    const double dn = (double)n;
+    const double mean = __ddiv_rn(s1, dn);
+    double v = __dsub_rn(__ddiv_rn(s2, dn), __dmul_rn(mean, mean));
+    if (v < 0.0) v = 0.0;
+    const int sl = page % META_TILE;
+    const long long T = ((long long)b * m.Hkv + kvh) * m.n_tiles + page / META_TILE;
+    const int ch = j / 16, e = j % 16;
+    uint8_t *bb = m.meta + T * 128 * D + ch * 2048;
+    const int ob = sl * 32 + 16 * ((e >> 3) ^ ((sl >> 2) & 1)) + 2 * (e & 7);
+    *reinterpret_cast<uint16_t *>(bb + ob) = bf16_down(mn);
+    *reinterpret_cast<uint16_t *>(bb + 1024 + ob) = bf16_up(mx);
+    uint8_t *mm = m.meta + m.n_tiles_total * 128 * D + T * 256 * D + ch * 4096;
+    const int om = sl * 64 + 16 * ((e >> 2) ^ ((sl >> 1) & 3)) + 4 * (e & 3);
+    *reinterpret_cast<float *>(mm + om) = (float)mean;
+    *reinterpret_cast<float *>(mm + 2048 + om) = (float)v;
+}
+
 template <int D, int P>
 __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_constant__ Kv4RowArgs a) {
     pdl_wait();
-    extern __shared__ float kval[];  // [P][D] dequantised keys (with metadata)
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, TILE = Kv4<D>::TILE, CODES = Kv4<D>::CODES;
+    __shared__ __align__(16) unsigned char image[P / 16 * TILE];  // the page's key tiles (with metadata)
+    __shared__ Stats<D> stats;
     PageJob j;
     if (!page_job<P>(a, blockIdx.x, j)) return;
     const int kvh = a.m.kv0 + blockIdx.y;
@@ -240,136 +280,128 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_cons
     unsigned char *kt = a.k4 + kv4_tile<D>(j.blk, a.m.Hkv, kvh, P, 0);
     unsigned char *vt = a.v4 + kv4_tile<D>(j.blk, a.m.Hkv, kvh, P, 0);
     const bool meta = a.m.meta != nullptr;
-    const uint16_t *kr = a.k_new + (j.row0 - j.t0) * a.stride + (size_t)kvh * D;  // row of slot 0
-    const uint16_t *vr = a.v_new + (j.row0 - j.t0) * a.stride + (size_t)kvh * D;
-    // the page's old keys, for the metadata
-    if (meta)
-        for (int t = warp; t < j.t0; t += RW_WARPS) {
-            const unsigned char *tile = kt + (t >> 4) * Kv4<D>::TILE;
-            unsigned c[CPL<D>];
-            split_k<D>(reinterpret_cast<const unsigned *>(tile), t & 15, c);
-            const unsigned pr =
-                reinterpret_cast<const unsigned *>(tile + Kv4<D>::CODES)[(t & 15) * Kv4<D>::NG + lane_group<D>()];
-#pragma unroll
-            for (int i = 0; i < CPL<D>; ++i)
-                kval[t * D + CPL<D> * lane + i] = __fmaf_rn(bf16lo(pr), (float)c[i], bf16hi(pr));
+    const int l = lane % LPR<D>, g = l >> 2, c = l & 3;  // the lane's coordinates are 16 l .. 16 l + 15
+    const uint16_t *kr = a.k_new + (j.row0 - j.t0) * a.stride + (size_t)kvh * D + 16 * l;  // of slot 0
+    const uint16_t *vr = a.v_new + (j.row0 - j.t0) * a.stride + (size_t)kvh * D + 16 * l;
+    Row16 k, v;
+    auto fetch = [&](int t) {
+        if (t >= j.t0 && t < j.t1) {
+            k.load(kr + t * a.stride);
+            v.load(vr + t * a.stride);
+        } else {
+            k.clear();
+            v.clear();
         }
-    for (int pair = (j.t0 >> 1) + warp; 2 * pair < j.t1; pair += RW_WARPS) {
-        const int t = 2 * pair;
-        const bool has0 = t >= j.t0, has1 = t + 1 < j.t1;  // at least one of the pair is new
-        float kx[2][CPL<D>] = {}, vx[2][CPL<D>] = {};
-        if (has0) {
-            load_row<D>(kr + t * a.stride, kx[0]);
-            load_row<D>(vr + t * a.stride, vx[0]);
-        }
-        if (has1) {
-            load_row<D>(kr + (t + 1) * a.stride, kx[1]);
-            load_row<D>(vr + (t + 1) * a.stride, vx[1]);
-        }
-        unsigned char *ktile = kt + (t >> 4) * Kv4<D>::TILE, *vtile = vt + (t >> 4) * Kv4<D>::TILE;
-        unsigned half[2] = {0u, 0u};
-        unsigned *vp = reinterpret_cast<unsigned *>(vtile + Kv4<D>::CODES);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (!(e ? has1 : has0)) continue;
-            write_key<D>(ktile, (t + e) & 15, kx[e], meta ? kval + (t + e) * D : nullptr);
-            unsigned c[CPL<D>];
-            float s, lo;
-            quantise<D>(vx[e], c, s, lo);
-            half[e] = join_v<D>(c);
-            if (group_leader<D>()) vp[((t + e) & 15) * Kv4<D>::NG + lane_group<D>()] = pack_params(s, lo);
-        }
-        constexpr int SH = D == 128 ? 1 : 2;
-        if (lane % SH == 0) {
-            unsigned *w = reinterpret_cast<unsigned *>(vtile) + kv4_vword<D>((t & 15) >> 1, lane / SH);
-            unsigned v = half[0] | (half[1] << 16);
-            if (!(has0 && has1)) {  // the other token of the pair keeps its half
-                const unsigned old = *w;
-                v = has0 ? (half[0] | (old & 0xffff0000u)) : ((half[1] << 16) | (old & 0xffffu));
+    };
+    const int first = j.t0 / RPW<D> + warp;
+    fetch(first * RPW<D> + lane / LPR<D>);
+    if (meta && j.t0 > 0) {  // the page's old tokens
+        for (int i = threadIdx.x; i < (j.t0 + 15) / 16 * TILE / 16; i += RW_THREADS) cp_async16(image + 16 * i, kt + 16 * i);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+    }
+    for (int q = first; q * RPW<D> < j.t1; q += RW_WARPS) {
+        const int t = q * RPW<D> + lane / LPR<D>, u = t & 15, pair = u >> 1;
+        const bool mine = t >= j.t0 && t < j.t1, other = (t ^ 1) >= j.t0 && (t ^ 1) < j.t1;
+        unsigned kw[2], vw[2];
+        const unsigned kp = quantise<true>(k, kw), vp = quantise<false>(v, vw);
+        // halves of value words: the even token's lane makes those of coordinates 0 to 7
+        const bool odd = t & 1;
+        const unsigned keep = odd ? vw[1] : vw[0];
+        const unsigned got = __shfl_xor_sync(FULL, odd ? vw[0] : vw[1], LPR<D>);
+        const int tile = (t >> 4) * TILE;
+        if (mine) {
+            const uint2 w = make_uint2(kw[0], kw[1]);
+            const int at = tile + 4 * (u * (D / 8) + c * WPL + 2 * g), pat = tile + CODES + 4 * (u * NG + g);
+            *reinterpret_cast<uint2 *>(kt + at) = w;
+            if (c == 0) {
+                *reinterpret_cast<unsigned *>(kt + pat) = kp;
+                *reinterpret_cast<unsigned *>(vt + pat) = vp;
             }
-            *w = v;
+            if (meta) {
+                *reinterpret_cast<uint2 *>(image + at) = w;
+                if (c == 0) *reinterpret_cast<unsigned *>(image + pat) = kp;
+            }
         }
+        if (mine || other) {
+            const unsigned lo = odd ? got : keep, hi = odd ? keep : got;  // of the even and of the odd token
+            uint2 w = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+            uint2 *to = reinterpret_cast<uint2 *>(
+                vt + tile + 4 * (pair * (D / 4) + ((2 * c + odd) ^ kv4_vswz<D>(pair)) * WPL + 2 * g));
+            if (!(mine && other)) {  // the other token of the pair keeps its half
+                const uint2 old = *to;
+                const unsigned mask = mine == odd ? 0xffff0000u : 0x0000ffffu;  // of the new one
+                w.x = (w.x & mask) | (old.x & ~mask);
+                w.y = (w.y & mask) | (old.y & ~mask);
+            }
+            *to = w;
+        }
+        fetch(t + RW_WARPS * RPW<D>);
     }
     if (!meta) return;
     __syncthreads();
-    const int c = threadIdx.x;
-    if (c >= D) return;
-    float mn = INFINITY, mx = -INFINITY;
-    bool nan = false;
-    double s1 = 0.0, s2 = 0.0;
-    for (int t = 0; t < j.n; ++t) {
-        const float x = kval[t * D + c];
-        nan |= x != x;
-        mn = fminf(mn, x);
-        mx = fmaxf(mx, x);
-        const double xd = (double)x;
-        s1 = __dadd_rn(s1, xd);
-        s2 = __fma_rn(xd, xd, s2);
-    }
-    const double dn = (double)j.n;
-    const double m = __ddiv_rn(s1, dn);
-    double v = __dsub_rn(__ddiv_rn(s2, dn), __dmul_rn(m, m));
-    if (v < 0.0) v = 0.0;
-    if (nan) mn = mx = __int_as_float(0x7fc00000);
-    const int sl = j.page % META_TILE;
-    const long long T = ((long long)j.b * a.m.Hkv + kvh) * a.m.n_tiles + j.page / META_TILE;
-    const int ch = c / 16, e = c % 16;
-    uint8_t *bb = a.m.meta + T * 128 * D + ch * 2048;
-    const int ob = sl * 32 + 16 * ((e >> 3) ^ ((sl >> 2) & 1)) + 2 * (e & 7);
-    *reinterpret_cast<uint16_t *>(bb + ob) = bf16_down(mn);
-    *reinterpret_cast<uint16_t *>(bb + 1024 + ob) = bf16_up(mx);
-    uint8_t *mm = a.m.meta + a.m.n_tiles_total * 128 * D + T * 256 * D + ch * 4096;
-    const int om = sl * 64 + 16 * ((e >> 2) ^ ((sl >> 1) & 3)) + 4 * (e & 3);
-    *reinterpret_cast<float *>(mm + om) = (float)m;
-    *reinterpret_cast<float *>(mm + 2048 + om) = (float)v;
+    build_record<D>(a.m, image, stats, j.b, kvh, j.page, j.n);
 }
 
-// The lane's values of a row, to fp32 or bf16.
-template <int D>
-__device__ __forceinline__ void store_row(void *out, long long at, int f32, const unsigned (&c)[CPL<D>], unsigned pr) {
-    const int lane = threadIdx.x & 31;
-    float x[CPL<D>];
-#pragma unroll
-    for (int i = 0; i < CPL<D>; ++i) x[i] = __fmaf_rn(bf16lo(pr), (float)c[i], bf16hi(pr));
+// 16 values to fp32 or bf16.
+__device__ __forceinline__ void store16(void *out, long long at, int f32, const float (&x)[16]) {
     if (f32) {
-        float *o = static_cast<float *>(out) + at + CPL<D> * lane;
-        if constexpr (D == 128) *reinterpret_cast<float4 *>(o) = make_float4(x[0], x[1], x[2], x[3]);
-        else *reinterpret_cast<float2 *>(o) = make_float2(x[0], x[1]);
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     } else {
-        uint16_t *o = static_cast<uint16_t *>(out) + at + CPL<D> * lane;
-        const unsigned w0 = (unsigned)f2bf(x[0]) | ((unsigned)f2bf(x[1]) << 16);
-        if constexpr (D == 128) {
-            const unsigned w1 = (unsigned)f2bf(x[2]) | ((unsigned)f2bf(x[3]) << 16);
-            *reinterpret_cast<uint2 *>(o) = make_uint2(w0, w1);
-        } else {
-            *reinterpret_cast<unsigned *>(o) = w0;
-        }
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
+        unsigned w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
 template <int D, int P>
 __global__ void __launch_bounds__(RW_THREADS) kv4_read_kernel(const __grid_constant__ Kv4RowArgs a) {
     pdl_wait();
+    constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, TILE = Kv4<D>::TILE, CODES = Kv4<D>::CODES;
     PageJob j;
     if (!page_job<P>(a, blockIdx.x, j)) return;
     const int kvh = a.m.kv0 + blockIdx.y;
-    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % LPR<D>, g = l >> 2, c = l & 3;
     const size_t page = kv4_tile<D>(j.blk, a.m.Hkv, kvh, P, 0);
-    for (int t = j.t0 + warp; t < j.t1; t += RW_WARPS) {
-        const size_t tile = page + (size_t)(t >> 4) * Kv4<D>::TILE;
-        const long long at = (j.row0 + t - j.t0) * a.stride + (long long)kvh * D;
-        const int p = (t & 15) * Kv4<D>::NG + lane_group<D>();
-        unsigned c[CPL<D>];
-        split_k<D>(reinterpret_cast<const unsigned *>(a.k4 + tile), t & 15, c);
-        store_row<D>(a.k_out, at, a.f32, c, reinterpret_cast<const unsigned *>(a.k4 + tile + Kv4<D>::CODES)[p]);
-        split_v<D>(reinterpret_cast<const unsigned *>(a.v4 + tile), t & 15, c);
-        store_row<D>(a.v_out, at, a.f32, c, reinterpret_cast<const unsigned *>(a.v4 + tile + Kv4<D>::CODES)[p]);
+    for (int t = j.t0 + warp * RPW<D> + lane / LPR<D>; t < j.t1; t += RW_WARPS * RPW<D>) {
+        const int u = t & 15, pair = u >> 1;
+        const size_t tile = page + (size_t)(t >> 4) * TILE;
+        const unsigned char *kt = a.k4 + tile, *vt = a.v4 + tile;
+        const uint2 kw = *reinterpret_cast<const uint2 *>(kt + 4 * (u * (D / 8) + c * WPL + 2 * g));
+        const unsigned kp = *reinterpret_cast<const unsigned *>(kt + CODES + 4 * (u * NG + g));
+        const unsigned vp = *reinterpret_cast<const unsigned *>(vt + CODES + 4 * (u * NG + g));
+        uint2 vw[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            vw[h] = *reinterpret_cast<const uint2 *>(
+                vt + 4 * (pair * (D / 4) + ((2 * c + h) ^ kv4_vswz<D>(pair)) * WPL + 2 * g));
+        const long long at = (j.row0 + t - j.t0) * a.stride + (long long)kvh * D + 16 * l;
+        float x[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+            x[n] = __fmaf_rn(bf16lo(kp), code_f32((n < 8 ? kw.x : kw.y) >> (16 * (n & 1) + 4 * ((n & 7) >> 1))), bf16hi(kp));
+        store16(a.k_out, at, a.f32, x);
+        const int sh = 16 * (t & 1);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            const uint2 w = vw[n >> 3];
+            x[n] = __fmaf_rn(bf16lo(vp), code_f32(((n & 4) ? w.y : w.x) >> (sh + 4 * (n & 3))), bf16hi(vp));
+        }
+        store16(a.v_out, at, a.f32, x);
     }
 }
 
 template <int D, int P>
 cudaError_t write_t(const Kv4RowArgs &a, dim3 grid, cudaStream_t st) {
-    return launch_pdl(kv4_write_kernel<D, P>, grid, dim3(RW_THREADS), a.m.meta ? (size_t)P * D * 4 : 0, st, a);
+    return launch_pdl(kv4_write_kernel<D, P>, grid, dim3(RW_THREADS), 0, st, a);
 }
 template <int D, int P>
 cudaError_t read_t(const Kv4RowArgs &a, dim3 grid, cudaStream_t st) {

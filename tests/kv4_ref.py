@@ -125,12 +125,14 @@ def record(x, P_tokens):
         u = np.ascontiguousarray(v, np.float32).view(np.uint32).astype(np.uint64)
         u = np.where(v < 0, u + 0xFFFF, u)
         return ((u >> 16) << 16).astype(np.uint32).view(np.float32)
-    n = x.shape[0]
-    s1 = np.zeros(x.shape[1])
-    s2 = np.zeros(x.shape[1])
-    for t in range(n):
-        s1 = s1 + x[t]
-        s2 = s2 + x[t] * x[t]
+    n, parts = x.shape[0], 1024 // x.shape[1]
+    s1 = s2 = 0.0
+    for p in range(parts):  # every parts-th token, then the partial sums in order
+        a, b = np.zeros(x.shape[1]), np.zeros(x.shape[1])
+        for t in range(p, n, parts):
+            a = a + x[t]
+            b = b + x[t] * x[t]
+        s1, s2 = (a, b) if p == 0 else (s1 + a, s2 + b)
     mean = s1 / n
     var = np.maximum(s2 / n - mean * mean, 0)
     return down(x.min(0)), -down(-x.max(0)), mean.astype(np.float32), var.astype(np.float32)
