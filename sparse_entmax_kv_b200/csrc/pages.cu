@@ -4,9 +4,13 @@
 // Which blocks are free follows from the page table alone: the rows' blocks
 // are marked in a bitmap (one bit a block), and one CTA turns the bitmap and
 // the rows' needs into a plan (prefix sums in row and block order, so nothing
-// depends on timing).  Moving the pages is then a copy of (src, dst) block
-// pairs in every buffer, bound by memory bandwidth: 16-byte loads, several in
-// flight a thread, pair x buffer x chunk spread over a persistent grid.
+// depends on timing).  A second launch carries the plan out: new rows,
+// metadata records, and the (src, dst) block pairs in every buffer, bound by
+// memory bandwidth: 16-byte loads, several in flight a thread, row x tile and
+// pair x buffer x chunk spread over a grid that fills the GPU.  With tables of
+// up to SMALL_TABLE entries the planning CTA marks the blocks itself, in
+// shared memory, and the two (grow: one) launches are all; larger ones are
+// marked by the whole GPU in two launches before the plan.
 #include <cstring>
 
 #include "../../include/entmaxkv_pages.h"
@@ -18,6 +22,9 @@ namespace ekv {
 namespace {
 
 constexpr int PL_NT = 1024;  // threads of the planning CTA
+constexpr int SMALL_TABLE = 65536;   // entries, and ...
+constexpr int SMALL_WORDS = 8192;    // ... words of the bitmap that it marks itself
+constexpr int SMALL_ROWS = 1024;     // rows whose plan stays in shared memory
 constexpr int MV_NT = 256;
 constexpr int MV_UNROLL = 8;
 constexpr long long MV_CHUNK = (long long)MV_NT * MV_UNROLL * 16;  // bytes a CTA moves at a time
@@ -28,6 +35,7 @@ struct PageArgs {
     int *table_out, *lens_out;
     int in_place;
     unsigned *bits;      // [words] blocks in use
+    int small;           // the planning CTA marks them itself
     int words;
     int *act;            // [B] parent each row really follows (-1: empty)
     int *fresh;          // [B] block of the row's copied page, -1 none left, -2 none needed
@@ -48,20 +56,37 @@ __global__ void clear_kernel(int *p, int n) {
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
 }
 
-// Marks the blocks of the rows (one CTA a row, then the held ones).
-__global__ void mark_kernel(const __grid_constant__ PageArgs a) {
-    pdl_wait();
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int n = row_pages(a, b);
-        for (int p = threadIdx.x; p < n; p += blockDim.x) {
-            const int blk = a.table_in[(size_t)b * a.max_pages + p];
-            if (block_ok(a, blk)) atomicOr(&a.bits[blk >> 5], 1u << (blk & 31));
-            else atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
-        }
+// Marks the blocks of the table's entries i0, i0 + step, ... and the held ones.
+__device__ __forceinline__ void mark_blocks(const PageArgs &a, unsigned *bits, int i0, int step) {
+    const long long n = (long long)a.B * a.max_pages;
+    const int cap = a.max_pages * a.P;
+#pragma unroll 4
+    for (long long i = i0; i < n; i += step) {
+        const int b = (int)(i / a.max_pages), p = (int)(i - (long long)b * a.max_pages);
+        const int len = __ldg(a.lens_in + b), blk = __ldg(a.table_in + i);
+        if (p == 0 && len > cap) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
+        if ((long long)p * a.P >= len) continue;
+        if (block_ok(a, blk)) atomicOr(&bits[blk >> 5], 1u << (blk & 31));
+        else atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
     }
     if (a.hold)
-        for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.num_blocks; i += gridDim.x * blockDim.x)
-            if (a.hold[i] > 0) atomicOr(&a.bits[i >> 5], 1u << (i & 31));
+        for (int i = i0; i < a.num_blocks; i += step)
+            if (a.hold[i] > 0) atomicOr(&bits[i >> 5], 1u << (i & 31));
+}
+__global__ void mark_kernel(const __grid_constant__ PageArgs a) {
+    pdl_wait();
+    mark_blocks(a, a.bits, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+// The bitmap of blocks in use, as the planning CTA has it: marked before, or
+// (small tables) marked here, in shared memory.
+__device__ unsigned *marked_bits(const PageArgs &a, unsigned *sh) {
+    if (!a.small) return a.bits;
+    for (int i = threadIdx.x; i < a.words; i += PL_NT) sh[i] = 0u;
+    __syncthreads();
+    mark_blocks(a, sh, threadIdx.x, PL_NT);
+    __syncthreads();
+    return sh;
 }
 
 __global__ void refs_kernel(const __grid_constant__ PageArgs a) {
@@ -94,15 +119,15 @@ __device__ __forceinline__ unsigned word_mask(const PageArgs &a, int w) {
     return left >= 32 ? 0xffffffffu : (1u << left) - 1u;
 }
 
-// The first `want` free blocks, ascending, into a.list; returns how many.
-__device__ int list_free(const PageArgs &a, long long want, int *sh) {
+// The first `want` free blocks, ascending, into list; returns how many.
+__device__ int list_free(const PageArgs &a, const unsigned *bits, long long want, int *list, int *sh) {
     long long found = 0;
     for (int w0 = 0; w0 < a.words && found < want; w0 += PL_NT) {
         const int w = w0 + threadIdx.x;
-        unsigned f = w < a.words ? ~a.bits[w] & word_mask(a, w) : 0u;
+        unsigned f = w < a.words ? ~bits[w] & word_mask(a, w) : 0u;
         int tot;
         long long at = found + block_excl_scan(__popc(f), sh, &tot);
-        for (; f && at < want; f &= f - 1u, ++at) a.list[at] = 32 * w + __ffs(f) - 1;
+        for (; f && at < want; f &= f - 1u, ++at) list[at] = 32 * w + __ffs(f) - 1;
         found += tot;
     }
     __syncthreads();  // the list is read by other threads of the CTA
@@ -111,7 +136,11 @@ __device__ int list_free(const PageArgs &a, long long want, int *sh) {
 
 __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant__ PageArgs a) {
     pdl_wait();
+    extern __shared__ unsigned map[];
     __shared__ int sh[72];
+    __shared__ int s_act[SMALL_ROWS], s_first[SMALL_ROWS], s_list[SMALL_ROWS];
+    const bool few = a.B <= SMALL_ROWS;
+    int *act = few ? s_act : a.act, *first = few ? s_first : a.first, *list = few ? s_list : a.list;
     for (int b = threadIdx.x; b < a.B; b += PL_NT) {
         int p = a.parent[b];
         bool bad = p < -1 || p >= a.B;
@@ -120,22 +149,24 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
             atomicOr(a.status, ENTMAXKV_STATUS_BAD_ROW);
             p = a.in_place ? b : -1;
         }
-        a.act[b] = p;
-        a.first[b] = 0x7fffffff;
+        act[b] = p;
+        if (few) a.act[b] = p;
+        first[b] = 0x7fffffff;
     }
+    const unsigned *bits = marked_bits(a, map);
     __syncthreads();
     // the parent's own row keeps the partial page, else the first child
     for (int b = threadIdx.x; b < a.B; b += PL_NT) {
-        const int p = a.act[b];
-        if (p >= 0) atomicMin(&a.first[p], p == b ? -1 : b);
+        const int p = act[b];
+        if (p >= 0) atomicMin(&first[p], p == b ? -1 : b);
     }
     __syncthreads();
     auto needs = [&](int b, int &src) {
         if (b >= a.B) return 0;
-        const int p = a.act[b];
+        const int p = act[b];
         if (p < 0) return 0;
-        const int L = seq_len_of(a.lens_in, p, a.P, a.max_pages, a.status);
-        if (L % a.P == 0 || a.first[p] == (p == b ? -1 : b)) return 0;
+        const int L = seq_len_of(a.lens_in, p, a.P, a.max_pages, nullptr);
+        if (L % a.P == 0 || first[p] == (p == b ? -1 : b)) return 0;
         src = a.table_in[(size_t)p * a.max_pages + L / a.P];
         return 1;
     };
@@ -145,7 +176,7 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
         block_excl_scan(needs(b0 + threadIdx.x, src), sh, &tot);
         want += tot;
     }
-    const int have = list_free(a, want, sh);
+    const int have = list_free(a, bits, want < a.num_blocks ? want : a.num_blocks, list, sh);
     int rank = 0, pairs = 0;
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
         const int b = b0 + threadIdx.x;
@@ -155,7 +186,7 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
         rank += tot;
         int blk = -2;
         if (need) {
-            blk = at < have ? a.list[at] : -1;
+            blk = at < have ? list[at] : -1;
             if (blk < 0) atomicOr(a.status, ENTMAXKV_STATUS_NO_BLOCK);
         }
         const bool copy = blk >= 0 && block_ok(a, src);
@@ -170,64 +201,19 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
     if (threadIdx.x == 0) *a.n_pairs = pairs;
 }
 
-// The new rows of the table, one CTA a row.
-__global__ void fork_rows_kernel(const __grid_constant__ PageArgs a) {
-    pdl_wait();
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int p = a.act[b];
-        if (a.in_place && p == b) continue;
-        int L = p >= 0 ? seq_len_of(a.lens_in, p, a.P, a.max_pages, nullptr) : 0;
-        const int fresh = a.fresh[b];
-        if (fresh == -1) L -= L % a.P;
-        const int n = n_pages_of(L, a.P);
-        for (int i = threadIdx.x; i < a.max_pages; i += blockDim.x) {
-            int blk = -1;
-            if (i < n) blk = fresh >= 0 && i == n - 1 ? fresh : a.table_in[(size_t)p * a.max_pages + i];
-            a.table_out[(size_t)b * a.max_pages + i] = blk;
-        }
-        if (threadIdx.x == 0) a.lens_out[b] = L;
-    }
-}
-
-struct MetaMove {
-    const char *in[ENTMAXKV_MAX_BUFFERS];
-    char *out[ENTMAXKV_MAX_BUFFERS];
-    const int *act, *lens;
-    int in_place, B, Hkv, d, P, max_pages, n_tiles;
-    long long n_tiles_total;
-};
-
-// Metadata tiles follow their rows: one CTA per (row, kv head) and buffer.
-__global__ void fork_meta_kernel(const __grid_constant__ MetaMove a) {
-    pdl_wait();
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
-    const int p = a.act[b];
-    if (p < 0 || (a.in_place && p == b)) return;
-    const int n = n_pages_of(seq_len_of(a.lens, p, a.P, a.max_pages, nullptr), a.P);
-    const int tiles = (n + META_TILE - 1) / META_TILE;
-    const char *in = a.in[blockIdx.y];
-    char *out = a.out[blockIdx.y];
-    const long long src = ((long long)p * a.Hkv + h) * a.n_tiles, dst = ((long long)b * a.Hkv + h) * a.n_tiles;
-#pragma unroll
-    for (int region = 0; region < 2; ++region) {
-        const long long tile = (region ? 256 : 128) * a.d, base = region ? a.n_tiles_total * 128 * a.d : 0;
-        const uint4 *s = reinterpret_cast<const uint4 *>(in + base + src * tile);
-        uint4 *o = reinterpret_cast<uint4 *>(out + base + dst * tile);
-        for (long long i = threadIdx.x; i < tiles * tile / 16; i += blockDim.x) o[i] = s[i];
-    }
-}
-
 __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant__ PageArgs a) {
     pdl_wait();
+    extern __shared__ unsigned map[];
     __shared__ int sh[72];
-    __shared__ long long s_at[PL_NT];
+    __shared__ long long s_sum[PL_NT / 32];
+    const unsigned *bits = marked_bits(a, map);
     const long long cap = (long long)a.max_pages * a.P;
     // pages sequence b needs, its pages and new length; -1: it does not grow
     auto need = [&](int b, int &n0, long long &L) {
         if (b >= a.B) return -1;
         const int add = a.n_add[b];
         if (add <= 0) return -1;
-        const int L0 = seq_len_of(a.lens_in, b, a.P, a.max_pages, a.status);
+        const int L0 = seq_len_of(a.lens_in, b, a.P, a.max_pages, nullptr);
         L = (long long)L0 + add;
         if (L > cap) {
             atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
@@ -236,37 +222,41 @@ __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant_
         n0 = n_pages_of(L0, a.P);
         return (int)((L + a.P - 1) / a.P) - n0;
     };
-    // inclusive sums of the needs in 64 bits (a round of PL_NT at a time)
-    auto scan64 = [&](long long v) {
-        s_at[threadIdx.x] = v;
-        __syncthreads();
-        for (int o = 1; o < PL_NT; o <<= 1) {
-            const long long x = threadIdx.x >= o ? s_at[threadIdx.x - o] : 0;
-            __syncthreads();
-            s_at[threadIdx.x] += x;
-            __syncthreads();
+    // inclusive sums in 64 bits, and their total
+    auto scan64 = [&](long long x, long long &total) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL, x, o);
+            if (lane >= o) x += y;
         }
-        const long long r = s_at[threadIdx.x];
-        return r;
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = x;
+        __syncthreads();
+        total = 0;
+#pragma unroll 4
+        for (int w = 0; w < PL_NT / 32; ++w) {
+            if (w < warp) x += s_sum[w];
+            total += s_sum[w];
+        }
+        return x;
     };
-    long long want = 0;
+    long long want = 0, tot;
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
         int n0;
         long long L;
-        scan64(max(0, need(b0 + threadIdx.x, n0, L)));
-        want += s_at[PL_NT - 1];
-        __syncthreads();
+        scan64(max(0, need(b0 + threadIdx.x, n0, L)), tot);
+        want += tot;
     }
-    const int have = list_free(a, want < a.num_blocks ? want : a.num_blocks, sh);
+    const int have = list_free(a, bits, want < a.num_blocks ? want : a.num_blocks, a.list, sh);
     long long used = 0;
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
         const int b = b0 + threadIdx.x;
         int n0 = 0;
         long long L = 0;
         const int k = need(b, n0, L);
-        const long long end = used + scan64(max(0, k));
-        used += s_at[PL_NT - 1];
-        __syncthreads();
+        const long long end = used + scan64(max(0, k), tot);
+        used += tot;
         if (k < 0) continue;
         if (end > have && k > 0) {
             atomicOr(a.status, ENTMAXKV_STATUS_NO_BLOCK);
@@ -279,14 +269,16 @@ __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant_
 
 __global__ void __launch_bounds__(PL_NT) plan_compact_kernel(const __grid_constant__ PageArgs a) {
     pdl_wait();
+    extern __shared__ unsigned map[];
     __shared__ int sh[72];
+    const unsigned *bits = marked_bits(a, map);
     int n = 0, n_live;
-    for (int w = threadIdx.x; w < a.words; w += PL_NT) n += __popc(a.bits[w]);
+    for (int w = threadIdx.x; w < a.words; w += PL_NT) n += __popc(bits[w]);
     block_excl_scan(n, sh, &n_live);
     int holes = 0, moves = 0;
     for (int w0 = 0; w0 < a.words; w0 += PL_NT) {
         const int w = w0 + threadIdx.x;
-        const unsigned live = w < a.words ? a.bits[w] : 0u;
+        const unsigned live = w < a.words ? bits[w] : 0u;
         const unsigned valid = w < a.words ? word_mask(a, w) : 0u;
         const int left = n_live - 32 * w;  // blocks of the word below n_live
         const unsigned low = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
@@ -295,13 +287,11 @@ __global__ void __launch_bounds__(PL_NT) plan_compact_kernel(const __grid_consta
         int m = moves + block_excl_scan(__popc(live & ~low), sh, &tm);
         for (unsigned f = ~live & valid & low; f; f &= f - 1u) a.pair_dst[h++] = 32 * w + __ffs(f) - 1;
         for (unsigned f = live & ~low; f; f &= f - 1u) a.pair_src[m++] = 32 * w + __ffs(f) - 1;
-        for (unsigned f = valid; f; f &= f - 1u) {
-            const int i = __ffs(f) - 1;
-            a.remap[32 * w + i] = ((live & low) >> i) & 1u ? 32 * w + i : -1;
-        }
         holes += th;
         moves += tm;
     }
+    for (int i = threadIdx.x; i < a.num_blocks; i += PL_NT)
+        if (i < n_live || !((bits[i >> 5] >> (i & 31)) & 1u)) a.remap[i] = (bits[i >> 5] >> (i & 31)) & 1u ? i : -1;
     __syncthreads();  // holes == moves: the pairs are complete
     for (int i = threadIdx.x; i < moves; i += PL_NT) a.remap[a.pair_src[i]] = a.pair_dst[i];
     if (threadIdx.x == 0) {
@@ -310,14 +300,91 @@ __global__ void __launch_bounds__(PL_NT) plan_compact_kernel(const __grid_consta
     }
 }
 
-__global__ void remap_rows_kernel(const __grid_constant__ PageArgs a) {
+// ------------------------------------------------------------ carrying it out
+
+// One row of the new table.
+__device__ __forceinline__ void fork_row(const PageArgs &a, int b) {
+    const int p = a.act[b];
+    if (a.in_place && p == b) return;
+    int L = p >= 0 ? seq_len_of(a.lens_in, p, a.P, a.max_pages, nullptr) : 0;
+    const int fresh = a.fresh[b];
+    if (fresh == -1) L -= L % a.P;
+    const int n = n_pages_of(L, a.P);
+    for (int i = threadIdx.x; i < a.max_pages; i += blockDim.x) {
+        int blk = -1;
+        if (i < n) blk = fresh >= 0 && i == n - 1 ? fresh : a.table_in[(size_t)p * a.max_pages + i];
+        a.table_out[(size_t)b * a.max_pages + i] = blk;
+    }
+    if (threadIdx.x == 0) a.lens_out[b] = L;
+}
+__device__ __forceinline__ void remap_row(const PageArgs &a, int b) {
+    const int n = n_pages_of(seq_len_of(a.lens_in, b, a.P, a.max_pages, nullptr), a.P);
+    for (int i = threadIdx.x; i < a.max_pages; i += blockDim.x) {
+        const size_t at = (size_t)b * a.max_pages + i;
+        const int blk = i < n ? a.table_in[at] : -1;
+        a.table_out[at] = block_ok(a, blk) ? a.remap[blk] : -1;
+    }
+}
+
+// Up to MV_CHUNK bytes (a multiple of 16), all loads before the stores.
+__device__ __forceinline__ void move_chunk(const char *from, char *to, long long bytes) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(from);
+    uint4 *dst = reinterpret_cast<uint4 *>(to);
+    const int m = (int)(bytes < MV_CHUNK ? bytes : MV_CHUNK) / 16;
+    uint4 v[MV_UNROLL];
+#pragma unroll
+    for (int u = 0; u < MV_UNROLL; ++u)
+        if (u * MV_NT + threadIdx.x < m) v[u] = src[u * MV_NT + threadIdx.x];
+#pragma unroll
+    for (int u = 0; u < MV_UNROLL; ++u)
+        if (u * MV_NT + threadIdx.x < m) dst[u * MV_NT + threadIdx.x] = v[u];
+}
+
+struct ApplyArgs {
+    PageArgs p;
+    int bufs, metas;
+    long long bytes;  // of a block
+    int Hkv, n_tiles;
+    long long region, tile[2];  // bytes of the bound region, and of a tile in it and in the other
+    char *buf[ENTMAXKV_MAX_BUFFERS];
+    const char *meta_in[ENTMAXKV_MAX_BUFFERS];
+    char *meta_out[ENTMAXKV_MAX_BUFFERS];
+};
+
+// Rows, then metadata tiles (of both regions; they follow their rows), then
+// chunks of the block pairs, item after item.
+template <bool FORK>
+__global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__ ApplyArgs a) {
     pdl_wait();
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int n = n_pages_of(seq_len_of(a.lens_in, b, a.P, a.max_pages, nullptr), a.P);
-        for (int i = threadIdx.x; i < a.max_pages; i += blockDim.x) {
-            const size_t at = (size_t)b * a.max_pages + i;
-            const int blk = i < n ? a.table_in[at] : -1;
-            a.table_out[at] = block_ok(a, blk) ? a.remap[blk] : -1;
+    const PageArgs &p = a.p;
+    const long long per = (a.bytes + MV_CHUNK - 1) / MV_CHUNK;  // chunks of a block
+    const long long meta0 = p.B, n_meta = FORK ? (long long)a.metas * p.B * a.Hkv * a.n_tiles : 0, move0 = meta0 + n_meta;
+    const long long total = move0 + per * a.bufs * (a.bufs ? *p.n_pairs : 0);
+    for (long long k = blockIdx.x; k < total; k += gridDim.x) {
+        if (k >= move0) {
+            const long long pb = (k - move0) / per, off = ((k - move0) - pb * per) * MV_CHUNK;
+            const int pair = (int)(pb / a.bufs);
+            char *base = a.buf[pb - (long long)pair * a.bufs] + off;
+            move_chunk(base + p.pair_src[pair] * a.bytes, base + p.pair_dst[pair] * a.bytes, a.bytes - off);
+        } else if (k >= meta0) {
+            long long i = k - meta0;
+            const int t = (int)(i % a.n_tiles);
+            i /= a.n_tiles;
+            const int h = (int)(i % a.Hkv);
+            i /= a.Hkv;
+            const int b = (int)(i % p.B), m = (int)(i / p.B), from = p.act[b];
+            if (from < 0 || (p.in_place && from == b)) continue;
+            if ((long long)t * META_TILE * p.P >= seq_len_of(p.lens_in, from, p.P, p.max_pages, nullptr)) continue;
+            const long long s = ((long long)from * a.Hkv + h) * a.n_tiles + t, d = ((long long)b * a.Hkv + h) * a.n_tiles + t;
+#pragma unroll 1
+            for (int r = 0; r < 2; ++r) {
+                const long long base = r ? a.region : 0;
+                move_chunk(a.meta_in[m] + base + s * a.tile[r], a.meta_out[m] + base + d * a.tile[r], a.tile[r]);
+            }
+        } else if (FORK) {
+            fork_row(p, (int)k);
+        } else {
+            remap_row(p, (int)k);
         }
     }
 }
@@ -326,7 +393,6 @@ struct MoveArgs {
     const char *src[ENTMAXKV_MAX_BUFFERS];
     char *dst[ENTMAXKV_MAX_BUFFERS];
     const int *src_ids, *dst_ids;
-    const int *n_dev;  // pairs, on the device (else n)
     int n, bufs, src_blocks, dst_blocks;
     long long bytes;   // of a block
     int *status;
@@ -335,29 +401,17 @@ struct MoveArgs {
 // Block pairs, every buffer: chunk after chunk of MV_CHUNK bytes.
 __global__ void __launch_bounds__(MV_NT) move_kernel(const __grid_constant__ MoveArgs a) {
     pdl_wait();
-    const int n = a.n_dev ? *a.n_dev : a.n;
     const long long per = (a.bytes + MV_CHUNK - 1) / MV_CHUNK;  // chunks of a block
-    const long long total = per * a.bufs * n;
+    const long long total = per * a.bufs * a.n;
     for (long long k = blockIdx.x; k < total; k += gridDim.x) {
-        const long long pb = k / per;
-        const int pair = (int)(pb / a.bufs), buf = (int)(pb % a.bufs);
+        const long long pb = k / per, off = (k - pb * per) * MV_CHUNK;
+        const int pair = (int)(pb / a.bufs), buf = (int)(pb - (long long)pair * a.bufs);
         const int s = a.src_ids[pair], d = a.dst_ids[pair];
         if (s < 0 || s >= a.src_blocks || d < 0 || d >= a.dst_blocks) {
             if (threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
             continue;
         }
-        const long long off = (k % per) * MV_CHUNK;
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.src[buf] + s * a.bytes + off);
-        uint4 *dst = reinterpret_cast<uint4 *>(a.dst[buf] + d * a.bytes + off);
-        const long long left = (a.bytes - off) / 16;
-        const int m = (int)(left < MV_CHUNK / 16 ? left : MV_CHUNK / 16);
-        uint4 v[MV_UNROLL];
-#pragma unroll
-        for (int u = 0; u < MV_UNROLL; ++u)
-            if (u * MV_NT + threadIdx.x < m) v[u] = src[u * MV_NT + threadIdx.x];
-#pragma unroll
-        for (int u = 0; u < MV_UNROLL; ++u)
-            if (u * MV_NT + threadIdx.x < m) dst[u * MV_NT + threadIdx.x] = v[u];
+        move_chunk(a.src[buf] + s * a.bytes + off, a.dst[buf] + d * a.bytes + off, a.bytes - off);
     }
 }
 
@@ -446,21 +500,46 @@ int on_device(PageArgs *a) {
 
 constexpr int GRID = 148 * 8;
 
-cudaError_t mark(const PageArgs &a, cudaStream_t st) {
-    cudaError_t e = launch_pdl(clear_kernel, dim3(min(ceil_div(a.words, 256), GRID)), dim3(256), 0, st,
-                               reinterpret_cast<int *>(a.bits), (int)a.words);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(mark_kernel, dim3(a.hold ? GRID : min(a.B, GRID)), dim3(256), 0, st, a);
+// The planning launch, after the marking ones where the table is large.
+template <class K>
+cudaError_t plan(K k, PageArgs &a, cudaStream_t st) {
+    const long long entries = (long long)a.B * a.max_pages;
+    a.small = entries <= SMALL_TABLE && a.words <= SMALL_WORDS;
+    if (!a.small) {
+        cudaError_t e = launch_pdl(clear_kernel, dim3(min(ceil_div(a.words, 256), GRID)), dim3(256), 0, st,
+                                   reinterpret_cast<int *>(a.bits), (int)a.words);
+        if (e != cudaSuccess) return e;
+        const long long items = a.hold && a.num_blocks > entries ? a.num_blocks : entries;
+        const long long ctas = (items + 255) / 256;
+        e = launch_pdl(mark_kernel, dim3((unsigned)(ctas < GRID ? ctas : GRID)), dim3(256), 0, st, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(k, dim3(1), dim3(PL_NT), a.small ? (size_t)a.words * 4 : 0, st, a);
 }
 
-void fill_move(MoveArgs *m, const entmaxkv_buffers *src, const entmaxkv_buffers *dst) {
-    *m = MoveArgs{};
-    m->bufs = src->count;
-    m->bytes = src->block_bytes;
-    for (int i = 0; i < src->count; ++i) {
-        m->src[i] = static_cast<const char *>(src->base[i]);
-        m->dst[i] = static_cast<char *>(dst->base[i]);
+// The second launch; pairs: how many blocks move at most.
+template <bool FORK>
+cudaError_t apply(const PageArgs &p, const entmaxkv_buffers *bufs, const entmaxkv_shape *s, long long pairs,
+                  const entmaxkv_buffers *meta_in, const entmaxkv_buffers *meta_out, cudaStream_t st) {
+    ApplyArgs a;
+    a.p = p;
+    a.bufs = bufs->count;
+    a.bytes = bufs->count ? bufs->block_bytes : 0;
+    for (int i = 0; i < bufs->count; ++i) a.buf[i] = static_cast<char *>(bufs->base[i]);
+    a.metas = meta_in ? meta_in->count : 0;
+    for (int i = 0; i < a.metas; ++i) {
+        a.meta_in[i] = static_cast<const char *>(meta_in->base[i]);
+        a.meta_out[i] = static_cast<char *>(meta_out->base[i]);
     }
+    a.Hkv = s->Hkv;
+    a.n_tiles = meta_tiles(s->max_pages);
+    a.tile[0] = 128ll * s->d;
+    a.tile[1] = 256ll * s->d;
+    a.region = (long long)s->B * s->Hkv * a.n_tiles * a.tile[0];
+    static_assert(256 * 128 <= MV_CHUNK, "a metadata tile is one chunk");
+    const long long items = s->B + (long long)a.metas * s->B * s->Hkv * a.n_tiles +
+                            (a.bytes + MV_CHUNK - 1) / MV_CHUNK * a.bufs * pairs;
+    return launch_pdl(apply_kernel<FORK>, dim3((unsigned)(items < GRID ? items : GRID)), dim3(MV_NT), 0, st, a);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
@@ -517,37 +596,8 @@ int entmaxkv_pages_fork(const entmaxkv_shape *s, const int32_t *parent, const in
     a.table_out = table_out;
     a.lens_out = lens_out;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = mark(a, st);
-    if (e == cudaSuccess) e = launch_pdl(plan_fork_kernel, dim3(1), dim3(PL_NT), 0, st, a);
-    if (e == cudaSuccess) e = launch_pdl(fork_rows_kernel, dim3(min(a.B, GRID)), dim3(256), 0, st, a);
-    if (e == cudaSuccess && bufs->count) {
-        MoveArgs m;
-        fill_move(&m, bufs, bufs);
-        m.src_ids = a.pair_src;
-        m.dst_ids = a.pair_dst;
-        m.n_dev = a.n_pairs;
-        m.src_blocks = m.dst_blocks = s->num_blocks;
-        m.status = a.status;
-        e = launch_pdl(move_kernel, dim3(GRID), dim3(MV_NT), 0, st, m);
-    }
-    if (e == cudaSuccess && meta_in && meta_in->count) {
-        MetaMove m{};
-        for (int i = 0; i < meta_in->count; ++i) {
-            m.in[i] = static_cast<const char *>(meta_in->base[i]);
-            m.out[i] = static_cast<char *>(meta_out->base[i]);
-        }
-        m.act = a.act;
-        m.lens = lens_in;
-        m.in_place = a.in_place;
-        m.B = s->B;
-        m.Hkv = s->Hkv;
-        m.d = s->d;
-        m.P = s->page_size;
-        m.max_pages = s->max_pages;
-        m.n_tiles = meta_tiles(s->max_pages);
-        m.n_tiles_total = (long long)s->B * s->Hkv * m.n_tiles;
-        e = launch_pdl(fork_meta_kernel, dim3(s->B * s->Hkv, meta_in->count), dim3(256), 0, st, m);
-    }
+    cudaError_t e = plan(plan_fork_kernel, a, st);
+    if (e == cudaSuccess) e = apply<true>(a, bufs, s, s->B, meta_in, meta_out, st);
     return rc_of(e);
 }
 
@@ -562,9 +612,7 @@ int entmaxkv_pages_grow(const entmaxkv_shape *s, const int32_t *n_add, const int
     a.table_out = page_table;
     a.lens_out = seq_lens;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = mark(a, st);
-    if (e == cudaSuccess) e = launch_pdl(plan_grow_kernel, dim3(1), dim3(PL_NT), 0, st, a);
-    return rc_of(e);
+    return rc_of(plan(plan_grow_kernel, a, st));
 }
 
 int entmaxkv_pages_compact(const entmaxkv_shape *s, const int32_t *table_in, const int32_t *seq_lens,
@@ -579,19 +627,8 @@ int entmaxkv_pages_compact(const entmaxkv_shape *s, const int32_t *table_in, con
     a.remap = remap;
     a.n_live = n_live;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = mark(a, st);
-    if (e == cudaSuccess) e = launch_pdl(plan_compact_kernel, dim3(1), dim3(PL_NT), 0, st, a);
-    if (e == cudaSuccess) e = launch_pdl(remap_rows_kernel, dim3(min(a.B, GRID)), dim3(256), 0, st, a);
-    if (e == cudaSuccess && bufs->count) {
-        MoveArgs m;
-        fill_move(&m, bufs, bufs);
-        m.src_ids = a.pair_src;
-        m.dst_ids = a.pair_dst;
-        m.n_dev = a.n_pairs;
-        m.src_blocks = m.dst_blocks = s->num_blocks;
-        m.status = a.status;
-        e = launch_pdl(move_kernel, dim3(GRID), dim3(MV_NT), 0, st, m);
-    }
+    cudaError_t e = plan(plan_compact_kernel, a, st);
+    if (e == cudaSuccess) e = apply<false>(a, bufs, s, s->num_blocks, nullptr, nullptr, st);
     return rc_of(e);
 }
 
@@ -606,7 +643,12 @@ int entmaxkv_pages_copy(const entmaxkv_buffers *src, int32_t src_blocks, const e
     DevInfo di;
     if ((rc = device_info(&di))) return rc;
     MoveArgs m;
-    fill_move(&m, src, dst);
+    m.bufs = src->count;
+    m.bytes = src->block_bytes;
+    for (int i = 0; i < src->count; ++i) {
+        m.src[i] = static_cast<const char *>(src->base[i]);
+        m.dst[i] = static_cast<char *>(dst->base[i]);
+    }
     m.src_ids = src_ids;
     m.dst_ids = dst_ids;
     m.n = n;

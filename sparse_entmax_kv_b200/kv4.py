@@ -54,13 +54,21 @@ def sized(t, shape, name):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def current(stream):
+    """The current device, and the stream to launch on (the current one, unless another is given)."""
+    device = torch._C._cuda_getDevice()
+    return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else nv._stream(stream)
+
+
 def arg(t, dtype, shape, name, device, pinned_ok=False):
     """Address of a contiguous tensor of this dtype and shape on the current device `device` (None stays None)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype == dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     p = nv._ptr(t, dtype, name, pinned_ok=pinned_ok)
     sized(t, shape, name)
     on_current_device(t)
@@ -95,6 +103,10 @@ def _cache_bytes(shape):
     return shape.num_blocks * shape.Hkv * shape.page_size * shape.d // 16 * 9
 
 
+def _meta_bytes(shape):
+    return shape.B * shape.Hkv * ((shape.max_pages + 31) // 32) * 384 * shape.d
+
+
 def _cache_args(shape, k4, v4, page_table, seq_lens, device):
     n = (_cache_bytes(shape),)
     return (arg(k4, torch.uint8, n, "k4", device), arg(v4, torch.uint8, n, "v4", device),
@@ -119,45 +131,45 @@ def _rows(shape, x, name, dtypes, pinned_ok):
     return x.data_ptr(), form[0] if n > 1 else row
 
 
-def _row_pair(shape, k, v, names, dtypes, row_start, pinned_ok=False):
+def _row_pair(shape, k, v, names, dtypes, row_start, stream, pinned_ok=False):
     pk, sk = _rows(shape, k, names[0], dtypes, pinned_ok)
     pv, sv = _rows(shape, v, names[1], dtypes, pinned_ok)
     n = k.shape[0]
     if n != v.shape[0] or sk != sv or k.dtype != v.dtype:
         raise ValueError(f"{names[0]} and {names[1]}: expected the same rows, strides and dtype")
-    device = torch.cuda.current_device()
+    device, stream = current(stream)
     for x in (k, v):
         if x.is_cuda and x.get_device() != device:
             on_current_device(x)
     if row_start is None and n != shape.B:
         raise ValueError(f"{names[0]}: one row a sequence ({shape.B}) without row_start, got {n}")
-    return pk, pv, sk, arg(row_start, torch.int32, (shape.B + 1,), "row_start", device), n, device
+    return pk, pv, sk, arg(row_start, torch.int32, (shape.B + 1,), "row_start", device), n, device, stream
 
 
 def entmaxkv_kv4_write(shape, k_new, v_new, row_start, page_table, seq_lens, k4, v4, meta=None, stream=None):
     """Rows bf16 [n, Hkv, d] (row b of every sequence b when row_start is None) into the cache, as the last tokens of
     their sequences; with meta, the records of the pages they touch.  Rows may be pinned host tensors."""
-    pk, pv, stride, ps, n, device = _row_pair(shape, k_new, v_new, ("k_new", "v_new"), (torch.bfloat16,), row_start,
-                                              True)
+    pk, pv, stride, ps, n, device, st = _row_pair(shape, k_new, v_new, ("k_new", "v_new"), (torch.bfloat16,), row_start,
+                                                  stream, True)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
-    m = None if meta is None else arg(meta, torch.uint8, (nv.meta_bytes(shape),), "meta", device)
+    m = None if meta is None else arg(meta, torch.uint8, (_meta_bytes(shape),), "meta", device)
     nv._check("entmaxkv_kv4_write", lib().entmaxkv_kv4_write(
-        C.byref(shape), pk, pv, stride, ps, n, pt, sl, c4k, c4v, m, nv._stream(stream)))
+        C.byref(shape), pk, pv, stride, ps, n, pt, sl, c4k, c4v, m, st))
 
 
 def entmaxkv_kv4_read(shape, k4, v4, row_start, page_table, seq_lens, k_out, v_out, stream=None):
     """The last tokens of every sequence into rows [n, Hkv, d], bf16 or fp32: the inverse of entmaxkv_kv4_write."""
-    pk, pv, stride, ps, n, device = _row_pair(shape, k_out, v_out, ("k_out", "v_out"), tuple(_ROWS), row_start)
+    pk, pv, stride, ps, n, device, st = _row_pair(shape, k_out, v_out, ("k_out", "v_out"), _ROWS, row_start, stream)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
     nv._check("entmaxkv_kv4_read", lib().entmaxkv_kv4_read(
-        C.byref(shape), c4k, c4v, stride, ps, n, pt, sl, _ROWS[k_out.dtype], pk, pv, nv._stream(stream)))
+        C.byref(shape), c4k, c4v, stride, ps, n, pt, sl, _ROWS[k_out.dtype], pk, pv, st))
 
 
 def entmaxkv_kv4_decode(shape, q, k4, v4, page_table, seq_lens, alpha, out, tau_out=None, sel=None, cnt=None, *,
                         workspace, stream=None):
     """Attention of q (bf16 [B, Hq, d]) over the 4-bit cache into out (fp32 [B, Hq, d]): softmax (alpha = 1) or
     alpha-entmax, over the selected pages, or over all of them without sel and cnt."""
-    device = torch.cuda.current_device()
+    device, st = current(stream)
     heads = (shape.B, shape.Hq)
     rows = heads + (shape.d,)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
@@ -168,4 +180,4 @@ def entmaxkv_kv4_decode(shape, q, k4, v4, page_table, seq_lens, alpha, out, tau_
         C.byref(shape), arg(q, torch.bfloat16, rows, "q", device), c4k, c4v, pt, sl,
         arg(sel, torch.int32, heads + (shape.max_pages,), "sel", device), arg(cnt, torch.int32, heads, "cnt", device),
         float(alpha), arg(out, torch.float32, rows, "out", device, pinned_ok=True),
-        arg(tau_out, torch.float32, heads, "tau_out", device), ws, workspace.numel(), nv._stream(stream)))
+        arg(tau_out, torch.float32, heads, "tau_out", device), ws, workspace.numel(), st))

@@ -12,7 +12,7 @@ import ctypes as C
 import torch
 
 from . import native as nv
-from .kv4 import arg, on_current_device
+from .kv4 import arg, current, on_current_device
 
 EXPORTED = ("entmaxkv_pages_workspace_size", "entmaxkv_pages_refs", "entmaxkv_pages_fork", "entmaxkv_pages_grow",
             "entmaxkv_pages_compact", "entmaxkv_pages_copy")
@@ -123,49 +123,53 @@ def _ws(workspace, device):
 
 def entmaxkv_pages_refs(shape, page_table, seq_lens, refs=None, n_free=None, hold=None, *, workspace, stream=None):
     """refs (int32 [num_blocks]): rows that reach each block, plus holds; n_free (int32 [1]): blocks without any."""
-    B, nb, dev = shape.B, shape.num_blocks, torch.cuda.current_device()
+    B, nb = shape.B, shape.num_blocks
+    dev, st = current(stream)
     nv._check("entmaxkv_pages_refs", lib().entmaxkv_pages_refs(
         C.byref(shape), _i32(page_table, (B, shape.max_pages), "page_table", dev),
         _i32(seq_lens, (B,), "seq_lens", dev), _i32(hold, (nb,), "hold", dev), _i32(refs, (nb,), "refs", dev),
-        _i32(n_free, (1,), "n_free", dev), *_ws(workspace, dev), nv._stream(stream)))
+        _i32(n_free, (1,), "n_free", dev), *_ws(workspace, dev), st))
 
 
 def entmaxkv_pages_fork(shape, parent, table_in, lens_in, table_out, lens_out, buffers, meta_in=None, meta_out=None,
                         hold=None, *, workspace, stream=None):
     """Row b of the new table continues row parent[b] of the old one (-1: empty); full pages are shared, partial last
     pages copied in every buffer; metadata buffers follow their rows.  In place when the out tensors are the in ones."""
-    B, table, dev = shape.B, (shape.B, shape.max_pages), torch.cuda.current_device()
+    B, table = shape.B, (shape.B, shape.max_pages)
+    dev, st = current(stream)
     nv._check("entmaxkv_pages_fork", lib().entmaxkv_pages_fork(
         C.byref(shape), _i32(parent, (B,), "parent", dev), _i32(table_in, table, "table_in", dev),
         _i32(lens_in, (B,), "lens_in", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
         _i32(table_out, table, "table_out", dev), _i32(lens_out, (B,), "lens_out", dev),
         _buffers(buffers, shape, "buffers", dev), _metas(meta_in, shape, "meta_in", dev),
-        _metas(meta_out, shape, "meta_out", dev), *_ws(workspace, dev), nv._stream(stream)))
+        _metas(meta_out, shape, "meta_out", dev), *_ws(workspace, dev), st))
 
 
 def entmaxkv_pages_grow(shape, n_add, page_table, seq_lens, hold=None, *, workspace, stream=None):
     """Sequence b grows by n_add[b] tokens, in place: new pages get the lowest free blocks."""
-    B, dev = shape.B, torch.cuda.current_device()
+    B = shape.B
+    dev, st = current(stream)
     nv._check("entmaxkv_pages_grow", lib().entmaxkv_pages_grow(
         C.byref(shape), _i32(n_add, (B,), "n_add", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
         _i32(page_table, (B, shape.max_pages), "page_table", dev), _i32(seq_lens, (B,), "seq_lens", dev),
-        *_ws(workspace, dev), nv._stream(stream)))
+        *_ws(workspace, dev), st))
 
 
 def entmaxkv_pages_compact(shape, table_in, seq_lens, table_out, buffers, remap, n_live, hold=None, *, workspace,
                            stream=None):
     """Used blocks move below n_live, their count; the table follows (table_out may be table_in)."""
-    table, nb, dev = (shape.B, shape.max_pages), (shape.num_blocks,), torch.cuda.current_device()
+    table, nb = (shape.B, shape.max_pages), (shape.num_blocks,)
+    dev, st = current(stream)
     nv._check("entmaxkv_pages_compact", lib().entmaxkv_pages_compact(
         C.byref(shape), _i32(table_in, table, "table_in", dev), _i32(seq_lens, (shape.B,), "seq_lens", dev),
         _i32(hold, nb, "hold", dev), _i32(table_out, table, "table_out", dev), _buffers(buffers, shape, "buffers", dev),
-        _i32(remap, nb, "remap", dev), _i32(n_live, (1,), "n_live", dev), *_ws(workspace, dev), nv._stream(stream)))
+        _i32(remap, nb, "remap", dev), _i32(n_live, (1,), "n_live", dev), *_ws(workspace, dev), st))
 
 
 def entmaxkv_pages_copy(src, dst, src_ids, dst_ids, stream=None):
     """Block dst_ids[i] of every dst buffer := block src_ids[i] of the src buffer of the same number.  Either side
     may be pinned host memory."""
-    dev = torch.cuda.current_device()
+    dev, st = current(stream)
     for b, name in ((src, "src"), (dst, "dst")):
         if not isinstance(b, Buffers):
             raise TypeError(f"{name}: expected pages.Buffers")
@@ -175,4 +179,4 @@ def entmaxkv_pages_copy(src, dst, src_ids, dst_ids, stream=None):
     ids = (src_ids.shape[0],)
     nv._check("entmaxkv_pages_copy", lib().entmaxkv_pages_copy(
         src.ref, src.num_blocks, dst.ref, dst.num_blocks, _i32(src_ids, ids, "src_ids", dev),
-        _i32(dst_ids, ids, "dst_ids", dev), ids[0], nv._stream(stream)))
+        _i32(dst_ids, ids, "dst_ids", dev), ids[0], st))
