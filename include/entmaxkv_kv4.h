@@ -93,7 +93,8 @@ ENTMAXKV_API size_t entmaxkv_kv4_workspace_size(const entmaxkv_shape *shape);
 
 /*
  * Decode attention over the 4-bit cache: for each (b, h), over the tokens T
- * of the pages sel[b][h][0..cnt[b][h]) (as entmaxkv_select writes them), or
+ * of the pages sel[b][h][0..cnt[b][h]) (ascending, as entmaxkv_select writes
+ * them; anything else sets ENTMAXKV_STATUS_BAD_SELECTION or counts once), or
  * over every token of the sequence when sel and cnt are both NULL,
  *   alpha > 1:  out = sum_T p_t v_t with the exact alpha-entmax weights of
  *               entmaxkv_decode_sparse; value rows without weight are not

@@ -66,13 +66,15 @@ struct Kv4DecodeArgs {
     const uint16_t *q;
     const uint8_t *k4, *v4;
     const int *page_table, *seq_lens;
-    const int *union_e, *union_blk, *union_cnt;  // null: every page
+    const int *union_e, *union_blk, *union_cnt;  // the pages of each group (G > 1 with a selection),
+    const int *sel, *cnt;                        // or of each head (G = 1); all null: every page
     float *out, *tau_out;
     float *part_o;        // [slots][G][d] softmax partials
     float2 *part_ml;      // [slots][G]
     float *cand_z;        // [B Hq][max_pages P]
     unsigned *cand_row;   // [B Hq][max_pages P]  blk P + slot
-    int2 *seg;            // [slots][G] candidates of a warp's share of a group, their max
+    int4 *seg;            // [slots][G] candidates of a warp's share of a group, their max, place of the first
+    int2 *slots;          // [B Hkv] first and last slot of the group's shares
     int *zmax;            // [B Hq] running max of a head's z (order-mapped), null: none kept
     int W;                // warps that share the tiles at most
     int ct, lc;           // tiles of a chunk (1 or 2), log2 of the chunks of a page
@@ -85,127 +87,118 @@ struct Kv4DecodeArgs {
 
 // --------------------------------------------------------------- the range of chunks
 
-// Entries of the range: the sequences (nk groups each), or the groups of the
-// selections' unions.
-__device__ __forceinline__ int n_entries(const Kv4DecodeArgs &a) { return a.union_e ? a.B * a.nk : a.B; }
+// Entries of the range: the sequences (nk groups each), or with selections the
+// groups themselves.
+__device__ __forceinline__ bool chosen(const Kv4DecodeArgs &a) { return a.union_e || a.sel; }
+__device__ __forceinline__ int n_entries(const Kv4DecodeArgs &a) { return chosen(a) ? a.B * a.nk : a.B; }
+__device__ __forceinline__ int groups_of_entry(const Kv4DecodeArgs &a) { return chosen(a) ? 1 : a.nk; }
 __device__ __forceinline__ int tokens_of(const Kv4DecodeArgs &a, int b) {
     const int s = __ldg(a.seq_lens + b), cap = a.max_pages * a.P;
     return s < 0 ? 0 : min(s, cap);
 }
 // Chunks of each group of entry i.
 __device__ __forceinline__ int entry_chunks(const Kv4DecodeArgs &a, int i) {
-    if (!a.union_e) return n_pages_of(tokens_of(a, i), a.P) << a.lc;
+    if (!chosen(a)) return n_pages_of(tokens_of(a, i), a.P) << a.lc;
     int b, kvh;
     group_of(i, a.kv0, a.nk, b, kvh);
-    return __ldg(a.union_cnt + b * a.Hkv + kvh) << a.lc;
+    if (a.union_e) return __ldg(a.union_cnt + b * a.Hkv + kvh) << a.lc;
+    return max(0, min(__ldg(a.cnt + b * a.Hq + kvh), n_pages_of(tokens_of(a, b), a.P))) << a.lc;  // G = 1
 }
-__device__ __forceinline__ int groups_of_entry(const Kv4DecodeArgs &a) { return a.union_e ? 1 : a.nk; }
-
-// Chunks before the entries of each thread of the CTA (thread i owns entries
-// i C .. i C + C - 1), and their total.
-template <int NT>
-struct Plan {
-    long long pre[NT + 1];
-    long long warp_sum[NT / 32];
-    __device__ void make(const Kv4DecodeArgs &a) {
-        const int n = n_entries(a), C = (n + NT - 1) / NT, m = groups_of_entry(a);
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        long long v = 0;
-        for (int i = threadIdx.x * C; i < min(n, (int)(threadIdx.x + 1) * C); ++i) v += (long long)entry_chunks(a, i) * m;
-        long long x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(FULL, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sum[warp] = x;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) x += warp_sum[w];
-        pre[threadIdx.x] = x - v;
-        if (threadIdx.x == NT - 1) pre[NT] = x;
-        __syncthreads();
-    }
-    __device__ long long total() const { return pre[NT]; }
-    // Warps that share the range: no more than its chunks, so that none is left without.
-    __device__ int warps(const Kv4DecodeArgs &a) const { return (int)min((long long)a.W, total()); }
-    __device__ long long first_of(const Kv4DecodeArgs &a, int w) const { return total() * w / warps(a); }
-    // First chunk of entry i.
-    __device__ long long start_of(const Kv4DecodeArgs &a, int i) const {
-        const int C = (n_entries(a) + NT - 1) / NT, m = groups_of_entry(a);
-        long long s = pre[i / C];
-        for (int k = i / C * C; k < i; ++k) s += (long long)entry_chunks(a, k) * m;
-        return s;
-    }
-};
 
 // One warp's share of one group's list.
 struct Share {
     int b, kvh, bk, g;  // g: group in the order of the range
     int U, seq;         // pages of the list, tokens of the sequence
     int first, last;    // chunks [first, last) of the list
+    int T;              // chunks of the whole list
 };
 
-// Walks the entries from chunk t on.
+// A warp's part of the range, from its first chunk on.  Every warp finds it by
+// itself: lane i sums entries i C .. i C + C - 1.
 struct Walk {
-    int i;            // entry
-    int T;            // chunks of each of its groups
-    long long start;  // its first chunk
-    template <int NT>
-    __device__ void to(const Kv4DecodeArgs &a, const Plan<NT> &p, long long t) {
-        int lo = 0, hi = NT - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.pre[mid] <= t) lo = mid;
-            else hi = mid - 1;
+    long long t, end;  // chunks [t, end) of the range are left
+    int i;             // entry of chunk t or before,
+    int T;             // the chunks of each of its groups,
+    long long start;   // its first chunk
+    __device__ __forceinline__ Walk(const Kv4DecodeArgs &a, int w) {
+        const int n = n_entries(a), C = (n + 31) / 32, m = groups_of_entry(a), lane = threadIdx.x & 31;
+        long long v = 0;
+#pragma unroll 4
+        for (int k = 0; k < C; ++k)
+            if (lane * C + k < n) v += entry_chunks(a, lane * C + k);
+        v *= m;
+        long long x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL, x, o);
+            if (lane >= o) x += y;
         }
-        start = p.pre[lo];
-        i = lo * ((n_entries(a) + NT - 1) / NT);
+        const long long total = __shfl_sync(FULL, x, 31);
+        x -= v;
+        // no more warps than chunks, so that every warp of them has one
+        const int W = (int)min((long long)a.W, total);
+        t = end = 0;
+        if (w >= W) return;
+        t = total * w / W;
+        end = total * (w + 1) / W;
+        const int l = __popc(__ballot_sync(FULL, x <= t)) - 1;
+        start = __shfl_sync(FULL, x, l);
+        i = l * C;
         T = entry_chunks(a, i);
     }
-    __device__ Share share(const Kv4DecodeArgs &a, long long t, long long end) {
+    __device__ __forceinline__ bool more() const { return t < end; }
+    __device__ __forceinline__ Share next(const Kv4DecodeArgs &a) {
         const int m = groups_of_entry(a);
         while (start + (long long)T * m <= t) {
             start += (long long)T * m;
             T = entry_chunks(a, ++i);
         }
-        const int sub = (int)((t - start) / T);
+        const int sub = m == 1 ? 0 : (int)(t - start) / T;
         Share s;
         s.g = i * m + sub;
         group_of(s.g, a.kv0, a.nk, s.b, s.kvh);
         s.bk = s.b * a.Hkv + s.kvh;
         s.U = T >> a.lc;
+        s.T = T;
         s.seq = tokens_of(a, s.b);
         const long long at = start + (long long)sub * T;
         s.first = (int)(t - at);
         s.last = (int)min((long long)T, s.first + (end - t));
+        t += s.last - s.first;
         return s;
     }
 };
 
-// Where the warps' shares of one group lie: slots w + g for w0 <= w <= w1
-// (w and g both ascend along the range, so no two shares meet in a slot).
-struct GroupSlots {
-    long long start;
-    int w0, w1, g;
-};
-template <int NT>
-__device__ GroupSlots group_slots(const Kv4DecodeArgs &a, const Plan<NT> &p, int b, int kvh) {
-    GroupSlots r;
-    r.g = b * a.nk + kvh - a.kv0;
-    const int i = a.union_e ? r.g : b;
-    const int T = entry_chunks(a, i);
-    r.w0 = 0;
-    r.w1 = -1;
-    if (T == 0) return r;
-    r.start = p.start_of(a, i) + (a.union_e ? 0 : (long long)(kvh - a.kv0) * T);
-    const long long W = p.warps(a), total = p.total();
-    r.w0 = (int)(((r.start + 1) * W - 1) / total);
-    r.w1 = (int)(((r.start + T) * W - 1) / total);
-    return r;
+// The shares of one group lie in consecutive slots w + g (w and g both ascend
+// along the range, so no two shares meet in a slot); the first and the last
+// one leave word of theirs.
+__device__ __forceinline__ void report_slot(const Kv4DecodeArgs &a, const Share &s, int w) {
+    if (s.first == 0) a.slots[s.bk].x = w + s.g;
+    if (s.last == s.T) a.slots[s.bk].y = w + s.g;
 }
+struct GroupShares {
+    size_t slot;  // of the first share
+    int n;
+};
 // The first slot of a call: every kv head has its own, for as many warps as a
 // call on it alone may use, so calls on disjoint ranges share a workspace.
 __host__ __device__ inline size_t slots_per_head(int B) { return (size_t)AT_MAX_WARPS + B; }
+
+// Called by every thread of a head's CTA; also reports what the host cannot see.
+__device__ __forceinline__ GroupShares group_shares(const Kv4DecodeArgs &a, int b, int kvh) {
+    const int2 s = __ldcg(a.slots + b * a.Hkv + kvh);
+    const int T = entry_chunks(a, chosen(a) ? b * a.nk + kvh - a.kv0 : b);
+    if (threadIdx.x == 0) {
+        const int len = __ldg(a.seq_lens + b);
+        if (len > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
+        if (a.sel && (unsigned)__ldg(a.cnt + b * a.Hq + kvh) > (unsigned)n_pages_of(tokens_of(a, b), a.P))
+            atomicOr(a.status, ENTMAXKV_STATUS_BAD_SELECTION);
+    }
+    GroupShares r;
+    r.n = T > 0 ? s.y - s.x + 1 : 0;
+    r.slot = a.kv0 * slots_per_head(a.B) + (T > 0 ? s.x : 0);
+    return r;
+}
 
 // --------------------------------------------------------------- the ring of tiles
 
@@ -245,7 +238,17 @@ struct TileRing {
         if (i >= s.U) return;
         int page = i, blk;
         mask = 0xff;
-        if (a.union_e) {
+        if (a.sel) {  // strictly ascending, or the entry is left out
+            const int *list = a.sel + (size_t)(s.b * a.Hq + s.kvh) * a.max_pages;
+            page = __ldg(list + i);
+            mask = 1;
+            if (page < 0 || page >= n_pages_of(s.seq, a.P) || (i > 0 && page <= __ldg(list + i - 1))) {
+                atomicOr(a.status, ENTMAXKV_STATUS_BAD_SELECTION);
+                return;
+            }
+            blk = __ldg(a.page_table + (size_t)s.b * a.max_pages + page);
+            if (blk < 0 || blk >= a.num_blocks) atomicOr(a.status, ENTMAXKV_STATUS_BAD_PAGE);
+        } else if (a.union_e) {
             const int ent = __ldg(a.union_e + (size_t)s.bk * a.max_pages + i);
             blk = __ldg(a.union_blk + (size_t)s.bk * a.max_pages + i);
             page = ent >> 8;
@@ -512,23 +515,17 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
     __shared__ int2 infos[AT_WARPS][RING_STAGES];
-    __shared__ Plan<AT_THREADS> plan;
-    plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
-    if (w >= plan.warps(a)) return;
     const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
     ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
-    long long t = plan.first_of(a, w);
-    const long long end = plan.first_of(a, w + 1);
-    Walk walk;
-    walk.to(a, plan, t);
-    while (t < end) {
-        const Share sh = walk.share(a, t, end);
-        t += sh.last - sh.first;
+    Walk walk(a, w);
+    bool alive = true;  // no wait ran out so far
+    while (walk.more()) {
+        const Share sh = walk.next(a);
         ring.start();
-        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
         Queries<D, G> Q;
         // z in powers of two
         Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, 1.4426950408889634f * rsqrtf((float)D));
@@ -542,12 +539,13 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
         // sums of p and of p (lo + 8 s) over the lane's tokens
         float ref[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, off[NG][2] = {};
         int until = FLUSH;
-        for (int i = sh.first; i < sh.last; ++i) {
+        for (int i = sh.first; i < sh.last && alive; ++i) {
             int2 what;
             unsigned char *stage;
             if (!ring.take(a, what, stage)) {
                 ring.drain(a);
-                return;
+                alive = false;  // the shares end empty, so that what reads them finds them whole
+                break;
             }
             const int mask = what.y >> 8;
             int n = what.y & 0xff;
@@ -688,6 +686,7 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
                 for (int g = 0; g < NG; ++g) off[g][e] += __shfl_xor_sync(FULL, off[g][e], o);
             }
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
+        if (lane == 0) report_slot(a, sh, w);
         if (r == 0)
 #pragma unroll
             for (int e = 0; e < NE; ++e)
@@ -726,7 +725,6 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     pdl_wait();
     constexpr int SUB = CB_NT / D;
     extern __shared__ float weight[];  // of each share
-    __shared__ Plan<CB_NT> plan;
     __shared__ float red[2][CB_NT / 32];
     __shared__ float o_sh[SUB][D];
     const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -734,13 +732,9 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     head_of(blockIdx.x, a.kv0 * G, a.nk * G, b, h);
     const int bh = b * a.Hq + h;
     const uint16_t qb = threadIdx.x < D ? a.q[(size_t)bh * D + threadIdx.x] : (uint16_t)0;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < a.B; i += CB_NT)
-            if (a.seq_lens[i] > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
-    plan.make(a);
-    const GroupSlots gs = group_slots(a, plan, b, h / G);
-    const int n = gs.w1 - gs.w0 + 1;
-    const size_t slot0 = a.kv0 * slots_per_head(a.B) + gs.w0 + gs.g;
+    const GroupShares gs = group_shares(a, b, h / G);
+    const int n = gs.n;
+    const size_t slot0 = gs.slot;
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
     float M = -INFINITY;
     for (int s = threadIdx.x; s < n; s += CB_NT) M = fmaxf(M, __ldcg(&a.part_ml[(slot0 + s) * G + h % G]).x);
@@ -809,24 +803,18 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     constexpr int EARLY = G == 8 ? 4 : 8;  // tiles a share begins with
     __shared__ float early[AT_WARPS][EARLY * 16 * G];
     __shared__ unsigned early_row[AT_WARPS][EARLY];
-    __shared__ Plan<AT_THREADS> plan;
-    plan.make(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
-    if (w >= plan.warps(a)) return;
     Ring ring;
     ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     const unsigned column = 0x11111111u << c, below = (1u << lane) - 1u;  // lanes of the same columns
     const size_t row_len = (size_t)a.max_pages * a.P;
-    long long t = plan.first_of(a, w);
-    const long long end = plan.first_of(a, w + 1);
-    Walk walk;
-    walk.to(a, plan, t);
-    while (t < end) {
-        const Share sh = walk.share(a, t, end);
-        t += sh.last - sh.first;
+    Walk walk(a, w);
+    bool alive = true;  // no wait ran out so far
+    while (walk.more()) {
+        const Share sh = walk.next(a);
         ring.start();
-        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last; ++i) ring.issue(a, sh, sh.first + i);
+        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
         const int h0 = sh.b * a.Hq + sh.kvh * G;
         Queries<D, G> Q;
         Q.load(a.q + (size_t)h0 * D, (a.alpha - 1.f) * rsqrtf((float)D));
@@ -902,12 +890,13 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
             }
             held = -1;
         };
-        for (int i = sh.first; i < sh.last; ++i) {
+        for (int i = sh.first; i < sh.last && alive; ++i) {
             int2 what;
             unsigned char *stage;
             if (!ring.take(a, what, stage)) {
                 ring.drain(a);
-                return;
+                alive = false;  // the shares end empty, so that what reads them finds them whole
+                break;
             }
             if (a.zmax && (i & 3) == 3) {  // used four chunks on: nothing waits for the load
 #pragma unroll
@@ -943,13 +932,14 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         }
         if (held >= 0) settle();
         const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
+        if (lane == 0) report_slot(a, sh, w);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
             // a NaN stays a candidate: its share may not be passed over for a low max
             if (__ballot_sync(FULL, bad[e]) & column) m[e] = __int_as_float(0x7fc00000);
-            if (r == 0 && 2 * c + e < G) a.seg[slot * G + 2 * c + e] = make_int2(n[e], __float_as_int(m[e]));
+            if (r == 0 && 2 * c + e < G) a.seg[slot * G + 2 * c + e] = make_int4(n[e], __float_as_int(m[e]), sh.first * (16 * a.ct), 0);
         }
     }
 }
@@ -969,8 +959,6 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     extern __shared__ int dyn[];
     float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates ...
     unsigned *crow = reinterpret_cast<unsigned *>(dyn + TK_CAP);    // [TK_CAP] ... and their value rows
-    int *seg_at = dyn + 2 * TK_CAP;                                 // [shares + 1] place of each share's candidates
-    __shared__ Plan<TK_NT> plan;
     __shared__ float o_sh[TK_NW][D];
     __shared__ float red[2][TK_NW][2];
     __shared__ float s_max[TK_NW];
@@ -983,20 +971,22 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const int bh = b * a.Hq + h, kvh = h / G;
     const float nan = __int_as_float(0x7fc00000);
     const uint16_t qb = threadIdx.x < D ? a.q[(size_t)bh * D + threadIdx.x] : (uint16_t)0;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < a.B; i += TK_NT)
-            if (a.seq_lens[i] > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
-    plan.make(a);
-    const GroupSlots gs = group_slots(a, plan, b, kvh);
-    const int W = gs.w1 - gs.w0 + 1;
-    const int2 *seg = a.seg + (a.kv0 * slots_per_head(a.B) + gs.w0 + gs.g) * G + h % G;
+    const GroupShares gs = group_shares(a, b, kvh);
+    const int W = gs.n;
+    int *seg_at = dyn + 2 * TK_CAP;                              // [W + 1] place of each share's candidates among the head's
+    int *seg_n = seg_at + W + 1, *seg_base = seg_n + W;          // [W] how many, and where their list starts
+    float *seg_max = reinterpret_cast<float *>(seg_base + W);    // [W] their largest
+    const int4 *seg = a.seg + gs.slot * G + h % G;
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
 
     float zmax = -INFINITY;
     int listed = 0;
     for (int i = threadIdx.x; i < W; i += TK_NT) {
-        const int2 s = __ldcg(seg + (size_t)i * G);
+        const int4 s = __ldcg(seg + (size_t)i * G);
+        seg_n[i] = s.x;
+        seg_max[i] = __int_as_float(s.y);
+        seg_base[i] = s.z;
         zmax = fmaxf(zmax, __int_as_float(s.y));
         listed |= s.x;
     }
@@ -1017,13 +1007,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const float thr = zmax - 1.f;
     const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
-    // first place of a share's list in the head's
-    auto seg_base = [&](int w) { return (int)max(0ll, plan.first_of(a, gs.w0 + w) - gs.start) * (16 * a.ct); };
     // listed candidates of a share that reaches the cut
-    auto seg_size = [&](int w) {
-        const int2 s = __ldcg(seg + (size_t)w * G);
-        return __int_as_float(s.y) <= thr ? 0 : s.x;
-    };
+    auto seg_size = [&](int w) { return seg_max[w] <= thr ? 0 : seg_n[w]; };
     // exclusive sums of f(w) over the shares, in seg_at; returns the total
     auto place = [&](auto f) {
         long long all = 0;
@@ -1047,7 +1032,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         for (int w = warp; w < W; w += TK_NW) {
             int at = seg_at[w];
             if (at == seg_at[w + 1]) continue;
-            const int n = seg_size(w), src = seg_base(w);
+            const int n = seg_size(w), src = seg_base[w];
             for (int i0 = 0; i0 < n; i0 += 32) {
                 const float z = i0 + lane < n ? __ldcg(zl + src + i0 + lane) : -INFINITY;
                 const bool keep = !(z <= thr);
@@ -1062,12 +1047,12 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         nc = 0;
         for (int base = 0; base < R; base += TK_NT * TK_EACH) {
             float z[TK_EACH];
-            int at[TK_EACH];
+            unsigned row[TK_EACH];
 #pragma unroll
             for (int u = 0; u < TK_EACH; ++u) {
                 const int i = base + u * TK_NT + threadIdx.x;
                 z[u] = -INFINITY;
-                at[u] = 0;
+                row[u] = 0u;
                 if (i < R) {
                     int lo = 0, hi = W - 1;
                     while (lo < hi) {
@@ -1075,8 +1060,9 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
                         if (seg_at[mid] <= i) lo = mid;
                         else hi = mid - 1;
                     }
-                    at[u] = seg_base(lo) + i - seg_at[lo];
-                    z[u] = __ldcg(zl + at[u]);
+                    const int at = seg_base[lo] + i - seg_at[lo];
+                    z[u] = __ldcg(zl + at);
+                    row[u] = __ldcg(rl + at);
                 }
             }
             unsigned keep[TK_EACH];
@@ -1105,7 +1091,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
                 const int k = nc + s_n[u * TK_NW + warp] + __popc(keep[u] & ((1u << lane) - 1u));
                 if (!(z[u] <= thr) && k < TK_CAP) {
                     cz[k] = z[u];
-                    crow[k] = __ldcg(rl + at[u]);
+                    crow[k] = row[u];
                 }
             }
             nc += s_n[32];
@@ -1117,7 +1103,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         // how many of each share stay, and where they go
         for (int w = warp; w < W; w += TK_NW) {
             const int n = seg_size(w);
-            const float *src = zl + seg_base(w);
+            const float *src = zl + seg_base[w];
             int k = 0;
             for (int i = lane; i < n; i += 32) k += !(__ldcg(src + i) <= thr);
 #pragma unroll
@@ -1163,9 +1149,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const int piece = ll / Kv4<D>::WPL, wi = ll % Kv4<D>::WPL;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const size_t rec = (size_t)(a.P / 16) * Kv4<D>::TILE;
-    auto add_row = [&](float z, unsigned row) {
-        const float p = pos_pow(z - tau, r, ri);
-        if (!(p > 0.f)) return;
+    auto add_row = [&](float p, unsigned row) {
         const unsigned blk = row / (unsigned)a.P;
         const int slot = (int)(row - blk * a.P), t = slot & 15, pair = t >> 1;
         const unsigned char *tile = a.v4 + ((size_t)blk * a.Hkv + kvh) * rec + (size_t)(slot >> 4) * Kv4<D>::TILE;
@@ -1180,16 +1164,39 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         for (int i = 0; i < 4; ++i) acc[i] += fmaf(s, (float)((w >> (4 * i)) & 15u), lo);
     };
     if (onchip) {
+        // the support alone, its weights and rows in place
+        int ns = 0;
+        for (int i0 = 0; i0 < nc; i0 += TK_NT) {
+            const int i = i0 + threadIdx.x;
+            const float p = i < nc ? pos_pow(cz[i] - tau, r, ri) : 0.f;
+            const unsigned row = i < nc ? crow[i] : 0u;
+            const unsigned keep = __ballot_sync(FULL, p > 0.f);
+            if (lane == 0) s_n[warp] = __popc(keep);
+            __syncthreads();
+            int at = ns;
+#pragma unroll
+            for (int w = 0; w < TK_NW; ++w) {
+                if (w < warp) at += s_n[w];
+                ns += s_n[w];
+            }
+            if (p > 0.f) {
+                at += __popc(keep & ((1u << lane) - 1u));
+                cz[at] = p;
+                crow[at] = row;
+            }
+            __syncthreads();
+        }
 #pragma unroll 4
-        for (int i = warp * RPW + sub; i < nc; i += TK_NW * RPW) add_row(cz[i], crow[i]);
+        for (int i = warp * RPW + sub; i < ns; i += TK_NW * RPW) add_row(cz[i], crow[i]);
     } else {
         for (int w = warp; w < W; w += TK_NW) {
             if (seg_at[w] == seg_at[w + 1]) continue;
-            const int n = seg_size(w), src = seg_base(w);
+            const int n = seg_size(w), src = seg_base[w];
 #pragma unroll 4
             for (int i = sub; i < n; i += RPW) {
                 const float z = __ldcg(zl + src + i);
-                if (z > tau) add_row(z, __ldcg(rl + src + i));
+                const float p = pos_pow(z - tau, r, ri);
+                if (p > 0.f) add_row(p, __ldcg(rl + src + i));
             }
         }
     }
@@ -1226,7 +1233,7 @@ int share_warps(const Kv4DecodeArgs &a, int sms, int ctas) {
 }
 
 struct Carve {
-    size_t part_o, part_ml, cand_z, cand_row, seg, union_e, union_blk, union_cnt, zmax, counters, total;
+    size_t part_o, part_ml, cand_z, cand_row, seg, slots, union_e, union_blk, union_cnt, zmax, counters, total;
 };
 
 Carve carve(const entmaxkv_shape *s) {
@@ -1244,7 +1251,8 @@ Carve carve(const entmaxkv_shape *s) {
     c.part_ml = take(rows * 8);
     c.cand_z = take(tokens * 4);
     c.cand_row = take(tokens * 4);
-    c.seg = take(rows * 8);
+    c.seg = take(rows * 16);
+    c.slots = take(groups * 8);
     c.union_e = take(groups * s->max_pages * 4);
     c.union_blk = take(groups * s->max_pages * 4);
     c.union_cnt = take(groups * 4);
@@ -1272,13 +1280,14 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
     }
     a.W = share_warps(a, sms, SCAN_CTAS);
     // short shares list little that a common max would have cut: no launch to reset it
-    if (!a.union_e && ((long long)a.B * a.nk * a.max_pages) << a.lc < 4ll * a.W) a.zmax = nullptr;
-    if (a.zmax && !a.union_e) {
+    const bool given = a.union_e;  // the union's kernel has reset it
+    if (!given && ((long long)a.B * a.nk * a.max_pages) << a.lc < 4ll * a.W) a.zmax = nullptr;
+    if (a.zmax && !given) {
         e = launch_pdl(kv4_reset_kernel, dim3(ceil_div(heads, 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
     if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
-    const size_t smem = (size_t)(2 * TK_CAP + a.W + 1) * 4;
+    const size_t smem = (size_t)(2 * TK_CAP + 4 * a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
     return launch_pdl(k, dim3(heads), dim3(TK_NT), smem, st, a);
@@ -1335,7 +1344,8 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.part_ml = reinterpret_cast<float2 *>(w + c.part_ml);
     a.cand_z = reinterpret_cast<float *>(w + c.cand_z);
     a.cand_row = reinterpret_cast<unsigned *>(w + c.cand_row);
-    a.seg = reinterpret_cast<int2 *>(w + c.seg);
+    a.seg = reinterpret_cast<int4 *>(w + c.seg);
+    a.slots = reinterpret_cast<int2 *>(w + c.slots);
     a.zmax = reinterpret_cast<int *>(w + c.zmax);
     a.B = s->B;
     a.Hq = s->Hq;
@@ -1350,7 +1360,10 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.r_int = alpha > 1.f ? integer_r(alpha) : 0;
     a.status = di.status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (sel) {
+    if (sel && s->Hq == s->Hkv) {  // a head's own list is its group's
+        a.sel = sel;
+        a.cnt = cnt;
+    } else if (sel) {
         DecodeArgs u;
         std::memset(&u, 0, sizeof(u));
         u.page_table = page_table;

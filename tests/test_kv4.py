@@ -439,6 +439,34 @@ def test_bad_pages_and_lengths_in_decode():
 
 @gpu
 @pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("G", [1, 2])
+def test_bad_selections(G, alpha):
+    """Entries outside the sequence are left out, entries given twice count once, counts beyond the pages are cut."""
+    c = Case(1, 2 * G, 2, 64, 16, [100])           # 7 pages
+    c.write(meta=False)
+
+    def run(entries, n):
+        sel = torch.full((1, 2 * G, c.mp), 5, dtype=torch.int32, device="cuda")
+        sel[0, :, :len(entries)] = torch.tensor(entries, dtype=torch.int32)
+        cnt = torch.full((1, 2 * G), n, dtype=torch.int32, device="cuda")
+        out, tau = c.decode(alpha, sel, cnt)
+        return out, tau, nv.get_status(clear=True)
+    nv.get_status(clear=True)
+    want = run([0, 2, 5], 3)
+    assert want[2] == 0
+    twice = run([0, 0, 2, 5, 5], 5)
+    assert twice[2] in (0, nv.STATUS_BAD_SELECTION)
+    beyond = run([-1, 0, 2, 5, 7], 5)
+    assert beyond[2] == nv.STATUS_BAD_SELECTION
+    for got in (twice, beyond):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    none = run([0], -3)
+    assert none[2] == nv.STATUS_BAD_SELECTION and (none[0] == 0).all() and none[1].isnan().all()
+    assert run(list(range(7)), 8)[2] & nv.STATUS_BAD_SELECTION
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
 def test_head_ranges_share_a_workspace_and_streams(alpha):
     """Calls on disjoint kv-head ranges on two streams at once, one workspace: the bits of one call."""
     c = Case(3, 12, 6, 64, 16, [900, 77, 2000])
