@@ -82,6 +82,7 @@ struct Kv4DecodeArgs {
     int kv0, nk;
     float alpha;
     int r_int;
+    unsigned one;         // 0x64006400: 1024 as two fp16, see code_f16
     int *status;
 };
 
@@ -314,17 +315,22 @@ struct TileRing {
 
 // --------------------------------------------------------------- operands
 
-// c - 8 of pair p of a word of eight codes (bits 4 p .. of each half), as two fp16.
+// c - 8 of pair p of a word of eight codes (bits 4 p .. of each half), as two
+// fp16.  one: 1024 twice, from a kernel argument: mask and or are one
+// instruction only while the compiler does not know both constants (with a
+// literal they were two; softmax over 8 x 32k tokens 84 us instead of 75).
 template <int p>
-__device__ __forceinline__ unsigned code_f16(unsigned w) {
+__device__ __forceinline__ unsigned code_f16(unsigned w, unsigned one) {
     const unsigned x = p < 2 ? w : w >> 8;
     unsigned y;
     if constexpr (p % 2 == 0)  // 1024 + c, less 1032
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"((x & 0x000f000fu) | 0x64006400u), "r"(0xe408e408u));
-    else  // 1024 + 16 c, over 16 and less 72
-        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000f000f, %2, 0xea;\n\tadd.rn.f16x2 %0, t, %3;\n\t}"
             : "=r"(y)
-            : "r"((x & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
+            : "r"(x), "r"(one), "r"(0xe408e408u));
+    else  // 1024 + 16 c, over 16 and less 72
+        asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00f000f0, %2, 0xea;\n\tfma.rn.f16x2 %0, t, %3, %4;\n\t}"
+            : "=r"(y)
+            : "r"(x), "r"(one), "r"(0x2c002c00u), "r"(0xd480d480u));
     return y;
 }
 // Two floats as fp16, x0 in the low half.
@@ -454,7 +460,8 @@ struct Params {
 // z of the 16 tokens of a tile: z[e] token lane / 4, z[2 + e] token lane / 4 +
 // 8, columns 2 (lane % 4) + e.
 template <int D, int G>
-__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D, G> &Q, float (&z)[4]) {
+__device__ __forceinline__ void tile_scores(const unsigned char *tile, const Queries<D, G> &Q, unsigned one,
+                                            float (&z)[4]) {
     constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, NE = Queries<D, G>::NE;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     unsigned w0[WPL], w1[WPL];
@@ -469,9 +476,9 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 2 * g; i < 2 * g + 2; ++i) {
-            mma_f16_16816(acc, code_f16<0>(w0[i]), code_f16<0>(w1[i]), code_f16<1>(w0[i]), code_f16<1>(w1[i]),
+            mma_f16_16816(acc, code_f16<0>(w0[i], one), code_f16<0>(w1[i], one), code_f16<1>(w0[i], one), code_f16<1>(w1[i], one),
                           Q.b[2 * i][0], Q.b[2 * i][1]);
-            mma_f16_16816(acc, code_f16<2>(w0[i]), code_f16<2>(w1[i]), code_f16<3>(w0[i]), code_f16<3>(w1[i]),
+            mma_f16_16816(acc, code_f16<2>(w0[i], one), code_f16<2>(w1[i], one), code_f16<3>(w0[i], one), code_f16<3>(w1[i], one),
                           Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
         }
 #pragma unroll
@@ -517,6 +524,7 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
     __shared__ int2 infos[AT_WARPS][RING_STAGES];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
+    const unsigned one = a.one;
     const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
     ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
@@ -552,7 +560,7 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
 #pragma unroll 1
             for (const unsigned char *tile = stage; n > 0; n -= 16, tile += Kv4<D>::TILE) {
                 float z[4], p[4], x[NG][4], y[NG][2];
-                tile_scores<D, G>(tile, Q, z);
+                tile_scores<D, G>(tile, Q, a.one, z);
                 const unsigned char *vt = tile + Ring::HALF;
                 Params<D> P;
                 P.load(vt);
@@ -651,12 +659,12 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
                     }
 #pragma unroll
                     for (int k = 2 * g; k < 2 * g + 2; ++k) {
-                        const unsigned a0 = code_f16<0>(w0[k]), a1 = code_f16<1>(w0[k]), a2 = code_f16<0>(w1[k]),
-                                       a3 = code_f16<1>(w1[k]);
+                        const unsigned a0 = code_f16<0>(w0[k], one), a1 = code_f16<1>(w0[k], one), a2 = code_f16<0>(w1[k], one),
+                                       a3 = code_f16<1>(w1[k], one);
 #pragma unroll
                         for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[q][0], bf[q][1]);
-                        const unsigned d0 = code_f16<2>(w0[k]), d1 = code_f16<3>(w0[k]), d2 = code_f16<2>(w1[k]),
-                                       d3 = code_f16<3>(w1[k]);
+                        const unsigned d0 = code_f16<2>(w0[k], one), d1 = code_f16<3>(w0[k], one), d2 = code_f16<2>(w1[k], one),
+                                       d3 = code_f16<3>(w1[k], one);
 #pragma unroll
                         for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[q][0], bf[q][1]);
                     }
@@ -912,7 +920,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
 #pragma unroll 1
             for (const unsigned char *tile = stage; left > 0; left -= 16, tile += Kv4<D>::TILE, row += 16) {
                 float z[4];
-                tile_scores<D, G>(tile, Q, z);
+                tile_scores<D, G>(tile, Q, a.one, z);
                 if (!whole<G>(mask, left)) mask_scores<G>(mask, left, z);
                 if (held < 0) {
                     test(z, row);
@@ -1358,6 +1366,7 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     a.lc = s->page_size == 64 ? 1 : 0;
     a.alpha = alpha;
     a.r_int = alpha > 1.f ? integer_r(alpha) : 0;
+    a.one = 0x64006400u;
     a.status = di.status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (sel && s->Hq == s->Hkv) {  // a head's own list is its group's
