@@ -60,7 +60,7 @@ constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a re
 // CTAs an SM holds (registers bound the softmax, shared memory allows five).
 template <int D, int G>
 constexpr int softmax_ctas() { return D == 64 && G < 8 ? 4 : 3; }
-constexpr int SCAN_CTAS = 5;
+constexpr int SCAN_CTAS = 4;
 
 struct Kv4DecodeArgs {
     const uint16_t *q;
@@ -981,10 +981,9 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const uint16_t qb = threadIdx.x < D ? a.q[(size_t)bh * D + threadIdx.x] : (uint16_t)0;
     const GroupShares gs = group_shares(a, b, kvh);
     const int W = gs.n;
-    int *seg_at = dyn + 2 * TK_CAP;                              // [W + 1] place of each share's candidates among the head's
-    int *seg_n = seg_at + W + 1, *seg_base = seg_n + W;          // [W] how many, and where their list starts
-    float *seg_max = reinterpret_cast<float *>(seg_base + W);    // [W] their largest
     const int4 *seg = a.seg + gs.slot * G + h % G;
+    int *seg_at = dyn + 2 * TK_CAP, *seg_base = seg_at + W + 1;  // place of each share's candidates among the head's, and
+                                                                 // in the head's list
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
 
@@ -992,9 +991,6 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     int listed = 0;
     for (int i = threadIdx.x; i < W; i += TK_NT) {
         const int4 s = __ldcg(seg + (size_t)i * G);
-        seg_n[i] = s.x;
-        seg_max[i] = __int_as_float(s.y);
-        seg_base[i] = s.z;
         zmax = fmaxf(zmax, __int_as_float(s.y));
         listed |= s.x;
     }
@@ -1016,7 +1012,11 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
     // listed candidates of a share that reaches the cut
-    auto seg_size = [&](int w) { return seg_max[w] <= thr ? 0 : seg_n[w]; };
+    auto seg_size = [&](int w) {
+        const int4 s = __ldcg(seg + (size_t)w * G);
+        seg_base[w] = s.z;
+        return __int_as_float(s.y) <= thr ? 0 : s.x;
+    };
     // exclusive sums of f(w) over the shares, in seg_at; returns the total
     auto place = [&](auto f) {
         long long all = 0;
@@ -1156,11 +1156,11 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const int ll = lane % LPR, sub = lane / LPR;
     const int piece = ll / Kv4<D>::WPL, wi = ll % Kv4<D>::WPL;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const size_t rec = (size_t)(a.P / 16) * Kv4<D>::TILE;
+    const size_t block = (size_t)(a.P / 16) * Kv4<D>::TILE;
     auto add_row = [&](float p, unsigned row) {
         const unsigned blk = row / (unsigned)a.P;
         const int slot = (int)(row - blk * a.P), t = slot & 15, pair = t >> 1;
-        const unsigned char *tile = a.v4 + ((size_t)blk * a.Hkv + kvh) * rec + (size_t)(slot >> 4) * Kv4<D>::TILE;
+        const unsigned char *tile = a.v4 + ((size_t)blk * a.Hkv + kvh) * block + (size_t)(slot >> 4) * Kv4<D>::TILE;
         // the lane's coordinate block keeps its place: read the word that holds it
         const unsigned w =
             __ldg(reinterpret_cast<const unsigned *>(tile) + pair * (D / 4) +
@@ -1295,7 +1295,7 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
-    const size_t smem = (size_t)(2 * TK_CAP + 4 * a.W + 1) * 4;
+    const size_t smem = (size_t)(2 * TK_CAP + 2 * a.W + 1) * 4;
     auto k = kv4_tau_kernel<D>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
     return launch_pdl(k, dim3(heads), dim3(TK_NT), smem, st, a);
