@@ -76,7 +76,8 @@ struct Kv4DecodeArgs {
     int4 *seg;            // [slots][G] candidates of a warp's share of a group, their max, place of the first
     int2 *slots;          // [B Hkv] first and last slot of the group's shares
     int *zmax;            // [B Hq] running max of a head's z (order-mapped), null: none kept
-    int W;                // warps that share the tiles at most
+    int W;                // warps that share the chunks at most
+    int S;                // with selections: shares of a group
     int ct, lc;           // tiles of a chunk (1 or 2), log2 of the chunks of a page
     int B, Hq, Hkv, P, max_pages, num_blocks;
     int kv0, nk;
@@ -112,16 +113,29 @@ struct Share {
     int U, seq;         // pages of the list, tokens of the sequence
     int first, last;    // chunks [first, last) of the list
     int T;              // chunks of the whole list
+    int slot;           // where what the share gives is kept: consecutive for the shares of a group
+    bool opens, closes; // its group's first, last share
 };
 
 // A warp's part of the range, from its first chunk on.  Every warp finds it by
-// itself: lane i sums entries i C .. i C + C - 1.
+// itself: lane i sums entries i C .. i C + C - 1.  The lists of selections are
+// about alike in length and may be many: there each group's list is cut in
+// a.S shares, and no warp has to know the other groups' (16 x 32 lists of 32
+// pages: 28 us for the scan with the range, see the table of times).
 struct Walk {
+    int w;             // the warp, or its next share
     long long t, end;  // chunks [t, end) of the range are left
     int i;             // entry of chunk t or before,
     int T;             // the chunks of each of its groups,
     long long start;   // its first chunk
     __device__ __forceinline__ Walk(const Kv4DecodeArgs &a, int w) {
+        this->w = w;
+        t = end = 0;
+        if (w >= a.W) return;
+        if (a.S) {
+            end = (long long)a.B * a.nk * a.S;  // shares
+            return;
+        }
         const int n = n_entries(a), C = (n + 31) / 32, m = groups_of_entry(a), lane = threadIdx.x & 31;
         long long v = 0;
 #pragma unroll 4
@@ -138,7 +152,6 @@ struct Walk {
         x -= v;
         // no more warps than chunks, so that every warp of them has one
         const int W = (int)min((long long)a.W, total);
-        t = end = 0;
         if (w >= W) return;
         t = total * w / W;
         end = total * (w + 1) / W;
@@ -147,8 +160,25 @@ struct Walk {
         i = l * C;
         T = entry_chunks(a, i);
     }
-    __device__ __forceinline__ bool more() const { return t < end; }
+    __device__ __forceinline__ bool more(const Kv4DecodeArgs &a) const { return a.S ? w < end : t < end; }
     __device__ __forceinline__ Share next(const Kv4DecodeArgs &a) {
+        if (a.S) {
+            Share s;
+            s.g = w / a.S;
+            const int k = w - s.g * a.S;
+            group_of(s.g, a.kv0, a.nk, s.b, s.kvh);
+            s.bk = s.b * a.Hkv + s.kvh;
+            s.T = entry_chunks(a, s.g);
+            s.U = s.T >> a.lc;
+            s.seq = tokens_of(a, s.b);
+            s.first = (int)((long long)s.T * k / a.S);
+            s.last = (int)((long long)s.T * (k + 1) / a.S);
+            s.slot = w;
+            s.opens = k == 0;
+            s.closes = k == a.S - 1;
+            w += a.W;
+            return s;
+        }
         const int m = groups_of_entry(a);
         while (start + (long long)T * m <= t) {
             start += (long long)T * m;
@@ -166,16 +196,18 @@ struct Walk {
         s.first = (int)(t - at);
         s.last = (int)min((long long)T, s.first + (end - t));
         t += s.last - s.first;
+        s.slot = w + s.g;
+        s.opens = s.first == 0;
+        s.closes = s.last == T;
         return s;
     }
 };
 
-// The shares of one group lie in consecutive slots w + g (w and g both ascend
-// along the range, so no two shares meet in a slot); the first and the last
-// one leave word of theirs.
-__device__ __forceinline__ void report_slot(const Kv4DecodeArgs &a, const Share &s, int w) {
-    if (s.first == 0) a.slots[s.bk].x = w + s.g;
-    if (s.last == s.T) a.slots[s.bk].y = w + s.g;
+// The shares of one group lie in consecutive slots, in the range w + g (both
+// ascend along it, so no two shares meet); the first and the last leave word.
+__device__ __forceinline__ void report_slot(const Kv4DecodeArgs &a, const Share &s) {
+    if (s.opens) a.slots[s.bk].x = s.slot;
+    if (s.closes) a.slots[s.bk].y = s.slot;
 }
 struct GroupShares {
     size_t slot;  // of the first share
@@ -393,26 +425,27 @@ struct Queries {
     unsigned b[D / 16][2];
     float sum[Kv4<D>::NG][NE];
     float factor[NE];
-    __device__ __forceinline__ void load(const uint16_t *q, float scale) {
+    __device__ __forceinline__ void fetch(const uint16_t *q) {
         const int lane = threadIdx.x & 31, c = lane & 3;
         const unsigned *qw = reinterpret_cast<const unsigned *>(q + (size_t)((lane >> 2) % G) * D);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) b[i][x] = __ldg(qw + 32 * (i >> 2) + 8 * c + 4 * ((i >> 1) & 1) + 2 * (i & 1) + x);
+    }
+    __device__ __forceinline__ void finish(float scale) {
+        const int lane = threadIdx.x & 31, c = lane & 3;
         float t[Kv4<D>::NG];
         unsigned top = 0;
 #pragma unroll
         for (int g = 0; g < Kv4<D>::NG; ++g) {
             t[g] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 4 * g; i < 4 * g + 4; ++i)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int j0 = 64 * g + 16 * c + 8 * i + 4 * k;
-                    unsigned *d = b[2 * (2 * g + i) + k];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        d[x] = qw[j0 / 2 + x];
-                        t[g] += bf16lo(d[x]) + bf16hi(d[x]);
-                        top = max(top, max((d[x] >> 7) & 0xffu, (d[x] >> 23) & 0xffu));  // exponent fields
-                    }
+                for (int x = 0; x < 2; ++x) {
+                    t[g] += bf16lo(b[i][x]) + bf16hi(b[i][x]);
+                    top = max(top, max((b[i][x] >> 7) & 0xffu, (b[i][x] >> 23) & 0xffu));  // exponent fields
                 }
             t[g] += __shfl_xor_sync(FULL, t[g], 1);
             t[g] += __shfl_xor_sync(FULL, t[g], 2);
@@ -530,13 +563,13 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
     ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     Walk walk(a, w);
     bool alive = true;  // no wait ran out so far
-    while (walk.more()) {
+    while (walk.more(a)) {
         const Share sh = walk.next(a);
+        Queries<D, G> Q;
+        Q.fetch(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D);
         ring.start();
         for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
-        Queries<D, G> Q;
-        // z in powers of two
-        Q.load(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D, 1.4426950408889634f * rsqrtf((float)D));
+        Q.finish(1.4426950408889634f * rsqrtf((float)D));  // z in powers of two
 
         float acc[MT][4], tot[MT][4];
 #pragma unroll
@@ -693,8 +726,8 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
 #pragma unroll
                 for (int g = 0; g < NG; ++g) off[g][e] += __shfl_xor_sync(FULL, off[g][e], o);
             }
-        const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
-        if (lane == 0) report_slot(a, sh, w);
+        const size_t slot = a.kv0 * slots_per_head(a.B) + sh.slot;
+        if (lane == 0) report_slot(a, sh);
         if (r == 0)
 #pragma unroll
             for (int e = 0; e < NE; ++e)
@@ -819,13 +852,14 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     const size_t row_len = (size_t)a.max_pages * a.P;
     Walk walk(a, w);
     bool alive = true;  // no wait ran out so far
-    while (walk.more()) {
+    while (walk.more(a)) {
         const Share sh = walk.next(a);
-        ring.start();
-        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
         const int h0 = sh.b * a.Hq + sh.kvh * G;
         Queries<D, G> Q;
-        Q.load(a.q + (size_t)h0 * D, (a.alpha - 1.f) * rsqrtf((float)D));
+        Q.fetch(a.q + (size_t)h0 * D);
+        ring.start();
+        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
+        Q.finish((a.alpha - 1.f) * rsqrtf((float)D));
         const size_t list = (size_t)(h0 + 2 * c) * row_len + (size_t)sh.first * (16 * a.ct);
 
         float m[2] = {-INFINITY, -INFINITY};      // the lane's max so far, of its columns
@@ -939,8 +973,8 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
             if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
         }
         if (held >= 0) settle();
-        const size_t slot = a.kv0 * slots_per_head(a.B) + w + sh.g;
-        if (lane == 0) report_slot(a, sh, w);
+        const size_t slot = a.kv0 * slots_per_head(a.B) + sh.slot;
+        if (lane == 0) report_slot(a, sh);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
 #pragma unroll
@@ -952,17 +986,19 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     }
 }
 
-constexpr int TK_NT = 256;
-constexpr int TK_NW = TK_NT / 32;
 constexpr int TK_CAP = 4096;   // candidates held on chip
-constexpr int TK_EACH = 4;     // listed ones a thread takes at a time ...
-constexpr int TK_FLAT = 32768; // ... of lists up to this long in all; longer ones go a warp a share
+constexpr int TK_PASS = 1024;  // listed ones that the CTA takes at a time
+constexpr int TK_BINS = 1024;
 
 // One CTA a head: the candidates above the head's max - 1 in token order, their
-// threshold, and the sum of p v over the support.
-template <int D>
+// threshold, and the sum of p v over the support.  Where more are listed than
+// fit on chip, a histogram of them first raises the cut: with every z of a bin
+// taken for its lower edge e, the largest edge t with sum (e - t)_+^r >= 1 is
+// below tau (alpha = 1.25 over 120k tokens: 1.7 ms without).
+template <int D, int TK_NT>
 __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
+    constexpr int TK_NW = TK_NT / 32, TK_EACH = TK_PASS / TK_NT;
     constexpr int NG = Kv4<D>::NG;
     extern __shared__ int dyn[];
     float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates ...
@@ -1008,7 +1044,9 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         return;
     }
 
-    const float thr = zmax - 1.f;
+    const float r = 1.f / (a.alpha - 1.f);
+    const int ri = a.r_int;
+    float thr = zmax - 1.f;  // nothing at or below it carries weight
     const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
     // listed candidates of a share that reaches the cut
@@ -1041,16 +1079,24 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             int at = seg_at[w];
             if (at == seg_at[w + 1]) continue;
             const int n = seg_size(w), src = seg_base[w];
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                const float z = i0 + lane < n ? __ldcg(zl + src + i0 + lane) : -INFINITY;
-                const bool keep = !(z <= thr);
-                const unsigned bal = __ballot_sync(FULL, keep);
-                if (keep) f(at + __popc(bal & ((1u << lane) - 1u)), z, src + i0 + lane);
-                at += __popc(bal);
+            for (int i0 = 0; i0 < n; i0 += 128) {
+                float z[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + 32 * u + lane;
+                    z[u] = i < n ? __ldcg(zl + src + i) : -INFINITY;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const bool keep = !(z[u] <= thr);
+                    const unsigned bal = __ballot_sync(FULL, keep);
+                    if (keep) f(at + __popc(bal & ((1u << lane) - 1u)), z[u], src + i0 + 32 * u + lane);
+                    at += __popc(bal);
+                }
             }
         }
     };
-    if (R <= TK_FLAT) {
+    if (R <= TK_CAP) {
         // the lists as one range, TK_EACH places a thread at a time
         nc = 0;
         for (int base = 0; base < R; base += TK_NT * TK_EACH) {
@@ -1097,7 +1143,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 #pragma unroll
             for (int u = 0; u < TK_EACH; ++u) {
                 const int k = nc + s_n[u * TK_NW + warp] + __popc(keep[u] & ((1u << lane) - 1u));
-                if (!(z[u] <= thr) && k < TK_CAP) {
+                if (!(z[u] <= thr)) {
                     cz[k] = z[u];
                     crow[k] = row[u];
                 }
@@ -1105,14 +1151,38 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             nc += s_n[32];
             __syncthreads();
         }
-        onchip = nc <= TK_CAP;
-    }
-    if (R > TK_FLAT || !onchip) {
+    } else {
+        int *bins = dyn;
+        for (int i = threadIdx.x; i < TK_BINS; i += TK_NT) bins[i] = 0;
+        __syncthreads();
+        each([&](int, float z, int) {
+            if (z == z) atomicAdd(&bins[min((int)((z - thr) * TK_BINS), TK_BINS - 1)], 1);
+        });
+        int lo = 0;
+        for (int top = TK_BINS - 1; lo < top;) {
+            const int mid = (lo + top + 1) >> 1;
+            __syncthreads();
+            float sum = 0.f;
+            for (int i = mid + threadIdx.x; i < TK_BINS; i += TK_NT)
+                sum += bins[i] * pos_pow((i - mid) * (1.f / TK_BINS), r, ri);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+            if (lane == 0) s_max[warp] = sum;
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < TK_NW; ++w) sum += s_max[w];
+            if (sum >= 1.001f) lo = mid;
+            else top = mid - 1;
+        }
+        __syncthreads();
+        thr = fmaxf(thr, thr + lo * (1.f / TK_BINS) - 1e-6f * fmaxf(1.f, fabsf(zmax)));
         // how many of each share stay, and where they go
         for (int w = warp; w < W; w += TK_NW) {
             const int n = seg_size(w);
             const float *src = zl + seg_base[w];
             int k = 0;
+#pragma unroll 4
             for (int i = lane; i < n; i += 32) k += !(__ldcg(src + i) <= thr);
 #pragma unroll
             for (int o = 16; o; o >>= 1) k += __shfl_xor_sync(FULL, k, o);
@@ -1135,8 +1205,6 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = nan;
         return;
     }
-    const float r = 1.f / (a.alpha - 1.f);
-    const int ri = a.r_int;
     const float hi = zmax - powf((float)nc, 1.f - a.alpha);
     float tau = thr;
     if (nc > 1 && hi > thr) {
@@ -1230,14 +1298,19 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 // Warps that share the chunks of a call over nk kv heads, on `ctas` CTAs an SM:
 // the grid fills the GPU once, unless that leaves fewer than AT_MIN_CHUNKS
 // chunks to a warp or cuts each group's list in more than AT_GROUP_PARTS.
-int share_warps(const Kv4DecodeArgs &a, int sms, int ctas) {
+void share_out(Kv4DecodeArgs &a, int sms, int ctas) {
     const long long groups = (long long)a.B * a.nk;
     const long long chunks = (groups * a.max_pages) << a.lc;
     long long W = (long long)sms * ctas * AT_WARPS;
     if (W > AT_MAX_WARPS) W = AT_MAX_WARPS;
     if (W > groups * AT_GROUP_PARTS) W = groups * AT_GROUP_PARTS;
     if (W > (chunks + AT_MIN_CHUNKS - 1) / AT_MIN_CHUNKS) W = (chunks + AT_MIN_CHUNKS - 1) / AT_MIN_CHUNKS;
-    return (int)W;
+    a.W = (int)W;
+    a.S = 0;
+    if (a.union_e || a.sel) {
+        a.S = (int)(W / groups > 1 ? W / groups : 1);
+        if (a.S * groups < W) a.W = (int)(a.S * groups);
+    }
 }
 
 struct Carve {
@@ -1281,12 +1354,12 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
     const int heads = a.B * a.nk * G;
     cudaError_t e;
     if (a.alpha == 1.f) {
-        a.W = share_warps(a, sms, softmax_ctas<D, G>());
+        share_out(a, sms, softmax_ctas<D, G>());
         e = run_shares(kv4_softmax_kernel<D, G>, a, AT_WARPS * TileRing<D, true>::BYTES, st);
         if (e != cudaSuccess) return e;
         return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(CB_NT), (size_t)a.W * 4, st, a);
     }
-    a.W = share_warps(a, sms, SCAN_CTAS);
+    share_out(a, sms, SCAN_CTAS);
     // short shares list little that a common max would have cut: no launch to reset it
     const bool given = a.union_e;  // the union's kernel has reset it
     if (!given && ((long long)a.B * a.nk * a.max_pages) << a.lc < 4ll * a.W) a.zmax = nullptr;
@@ -1296,9 +1369,12 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
     }
     if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
     const size_t smem = (size_t)(2 * TK_CAP + 2 * a.W + 1) * 4;
-    auto k = kv4_tau_kernel<D>;
+    // More threads a head while every head's CTA finds a place at once (128
+    // heads: 22 us with 512 threads, 25 with 256; 512 heads: 19 and 11)
+    const bool many = heads > 2 * sms;
+    auto k = many ? kv4_tau_kernel<D, 256> : kv4_tau_kernel<D, 512>;
     if ((e = ensure_smem(reinterpret_cast<const void *>(k), smem)) != cudaSuccess) return e;
-    return launch_pdl(k, dim3(heads), dim3(TK_NT), smem, st, a);
+    return launch_pdl(k, dim3(heads), dim3(many ? 256 : 512), smem, st, a);
 }
 
 template <int D>

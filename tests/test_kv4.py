@@ -352,7 +352,7 @@ def test_large_supports(alpha):
 @pytest.mark.parametrize("alpha", [1.0, 1.5])
 def test_scores_and_selection_run_on_the_4bit_metadata(alpha):
     """The bound of the 4-bit keys' metadata bounds every score, and a selection by it that keeps every page gives the
-    full result to the bit."""
+    full result (lists of selections are cut among the warps in another way, so the sums are not the same to the bit)."""
     c = Case(2, 8, 2, 128, 32, [333, 64])
     c.write()
     bbox = torch.full((2, 8, c.mp), -1e30, device="cuda")
@@ -361,9 +361,8 @@ def test_scores_and_selection_run_on_the_4bit_metadata(alpha):
     cnt = torch.empty((2, 8), dtype=torch.int32, device="cuda")
     nv.entmaxkv_select(c.shape, c.seq, bbox, None, None, nv.TOPK, c.mp, alpha, 0.0, sel, cnt)
     assert cnt.cpu().tolist() == [[11] * 8, [2] * 8]
-    all_out, all_tau = c.decode(alpha)
-    out, tau = c.decode(alpha, sel, cnt)
-    assert torch.equal(out, all_out) and torch.equal(tau, all_tau)
+    c.check_decode(alpha, *c.decode(alpha))
+    c.check_decode(alpha, *c.decode(alpha, sel, cnt), sel, cnt)
     q, bound = f64_of(c.q), f64_of(bbox)
     for b in range(2):
         K = ref.values(*ref.quantise(f64_of(c.k[c.rows_of(b)])))
