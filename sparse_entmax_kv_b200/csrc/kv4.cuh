@@ -52,6 +52,7 @@ struct Kv4RowArgs {
     uint8_t *k4, *v4;
     MetaArgs m;  // metadata (m.meta null: none), shape fields, kv-head range, status
     int f32;     // read: fp32 rows
+    unsigned big;  // the bits of 2^23
 };
 cudaError_t launch_kv4_write(const Kv4RowArgs &a, cudaStream_t st);
 cudaError_t launch_kv4_read(const Kv4RowArgs &a, cudaStream_t st);

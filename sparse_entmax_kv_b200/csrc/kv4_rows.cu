@@ -187,8 +187,31 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
-// A code (the low 4 bits) as a float: 2^23 + c, less 2^23.
-__device__ __forceinline__ float code_f32(unsigned c) { return __uint_as_float((c & 15u) | 0x4b000000u) - 8388608.f; }
+// The code at bits K .. K + 3 (K <= 16) of w, times 2^K, as a float: 2^23 + c
+// 2^K, less 2^23.  big: the bits of 2^23, from a kernel argument, so that mask
+// and or are one instruction (see code_f16 of the attention kernels).
+template <int K>
+__device__ __forceinline__ float code_f32(unsigned w, unsigned big) {
+    unsigned x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "n"(15 << K), "r"(big));
+    return __uint_as_float(x) - 8388608.f;
+}
+// The parameters of a row's group: s, s / 16, s / 256 and s / 4096 (exact) and
+// lo.  s / 2^K times a code times 2^K is the definition's product.
+struct Scales {
+    float s[4], lo;
+    __device__ __forceinline__ explicit Scales(unsigned pr) {
+        s[0] = bf16lo(pr);
+        lo = bf16hi(pr);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) s[i] = s[i - 1] * 0.0625f;
+    }
+    // Value of the code at bits 4 I of w.
+    template <int I>
+    __device__ __forceinline__ float at(unsigned w, unsigned big) const {
+        return __fmaf_rn(s[I], code_f32<4 * I>(w, big), lo);
+    }
+};
 
 // The metadata record of a page from its key tiles in shared memory.  A thread
 // takes four coordinates (half a word, one pair of parameters a token), so
@@ -202,7 +225,7 @@ struct Stats {
 };
 template <int D>
 __device__ __forceinline__ void build_record(const MetaArgs &m, const unsigned char *image, Stats<D> &sh, int b, int kvh,
-                                             int page, int n) {
+                                             int page, int n, unsigned big) {
     constexpr int PARTS = Stats<D>::PARTS;
     {
         const int q = threadIdx.x % (D / 4), part = threadIdx.x / (D / 4);
@@ -220,9 +243,12 @@ __device__ __forceinline__ void build_record(const MetaArgs &m, const unsigned c
         for (int t = part; t < n; t += PARTS) {
             const unsigned *tile = words + (t >> 4) * (Kv4<D>::TILE / 4);
             const unsigned w = tile[at + (t & 15) * (D / 8)] >> shift, pr = tile[pat + (t & 15) * Kv4<D>::NG];
+            const float s0 = bf16lo(pr), s1x = s0 * 0.0625f, lo = bf16hi(pr);
+            const float v[4] = {__fmaf_rn(s0, code_f32<0>(w, big), lo), __fmaf_rn(s0, code_f32<0>(w >> 16, big), lo),
+                                __fmaf_rn(s1x, code_f32<4>(w, big), lo), __fmaf_rn(s1x, code_f32<4>(w >> 16, big), lo)};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = __fmaf_rn(bf16lo(pr), code_f32(w >> (16 * (i & 1) + 4 * (i >> 1))), bf16hi(pr));
+                const float x = v[i];
                 mn[i] = min_nan(mn[i], x);
                 mx[i] = max_nan(mx[i], x);
                 const double xd = (double)x;
@@ -341,7 +367,7 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_cons
     }
     if (!meta) return;
     __syncthreads();
-    build_record<D>(a.m, image, stats, j.b, kvh, j.page, j.n);
+    build_record<D>(a.m, image, stats, j.b, kvh, j.page, j.n, a.big);
 }
 
 // 16 values to fp32 or bf16.
@@ -385,16 +411,23 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_read_kernel(const __grid_const
                 vt + 4 * (pair * (D / 4) + ((2 * c + h) ^ kv4_vswz<D>(pair)) * WPL + 2 * g));
         const long long at = (j.row0 + t - j.t0) * a.stride + (long long)kvh * D + 16 * l;
         float x[16];
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-            x[n] = __fmaf_rn(bf16lo(kp), code_f32((n < 8 ? kw.x : kw.y) >> (16 * (n & 1) + 4 * ((n & 7) >> 1))), bf16hi(kp));
+        const Scales ks(kp), vs(vp);
+        auto half = [&](unsigned w, const Scales &sc, float *x, int step) {  // four codes of 16 bits
+            x[0] = sc.template at<0>(w, a.big);
+            x[step] = sc.template at<1>(w, a.big);
+            x[2 * step] = sc.template at<2>(w, a.big);
+            x[3 * step] = sc.template at<3>(w, a.big);
+        };
+        half(kw.x, ks, x, 2);
+        half(kw.x >> 16, ks, x + 1, 2);
+        half(kw.y, ks, x + 8, 2);
+        half(kw.y >> 16, ks, x + 9, 2);
         store16(a.k_out, at, a.f32, x);
         const int sh = 16 * (t & 1);
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-            const uint2 w = vw[n >> 3];
-            x[n] = __fmaf_rn(bf16lo(vp), code_f32(((n & 4) ? w.y : w.x) >> (sh + 4 * (n & 3))), bf16hi(vp));
-        }
+        half(vw[0].x >> sh, vs, x, 1);
+        half(vw[0].y >> sh, vs, x + 4, 1);
+        half(vw[1].x >> sh, vs, x + 8, 1);
+        half(vw[1].y >> sh, vs, x + 12, 1);
         store16(a.v_out, at, a.f32, x);
     }
 }
@@ -450,6 +483,7 @@ int fill_rows(const entmaxkv_shape *s, const void *k_rows, const void *v_rows, i
     DevInfo di;
     if ((rc = device_info(&di))) return rc;
     *a = Kv4RowArgs{};
+    a->big = 0x4b000000u;
     a->stride = row_stride;
     a->row_start = row_start;
     a->n_rows = n_rows;
