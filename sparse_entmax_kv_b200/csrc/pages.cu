@@ -23,7 +23,7 @@ namespace {
 
 constexpr int PL_NT = 1024;  // threads of the planning CTA
 constexpr int SMALL_TABLE = 65536;   // entries, and ...
-constexpr int SMALL_WORDS = 8192;    // ... words of the bitmap that it marks itself
+constexpr int SMALL_WORDS = 7168;    // ... words of the bitmap that it marks itself (28 KB, beside 17 KB of plan)
 constexpr int SMALL_ROWS = 1024;     // rows whose plan stays in shared memory
 constexpr int MV_NT = 256;
 constexpr int MV_UNROLL = 8;
@@ -57,12 +57,14 @@ __global__ void clear_kernel(int *p, int n) {
 }
 
 // Marks the blocks of the table's entries i0, i0 + step, ... and the held ones.
+// I: 32 bits where the table is small (an entry's row is a division).
+template <class I>
 __device__ __forceinline__ void mark_blocks(const PageArgs &a, unsigned *bits, int i0, int step) {
-    const long long n = (long long)a.B * a.max_pages;
+    const I n = (I)a.B * (I)a.max_pages;
     const int cap = a.max_pages * a.P;
 #pragma unroll 4
-    for (long long i = i0; i < n; i += step) {
-        const int b = (int)(i / a.max_pages), p = (int)(i - (long long)b * a.max_pages);
+    for (I i = i0; i < n; i += step) {
+        const int b = (int)(i / (unsigned)a.max_pages), p = (int)(i - (I)b * (unsigned)a.max_pages);
         const int len = __ldg(a.lens_in + b), blk = __ldg(a.table_in + i);
         if (p == 0 && len > cap) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
         if ((long long)p * a.P >= len) continue;
@@ -75,7 +77,7 @@ __device__ __forceinline__ void mark_blocks(const PageArgs &a, unsigned *bits, i
 }
 __global__ void mark_kernel(const __grid_constant__ PageArgs a) {
     pdl_wait();
-    mark_blocks(a, a.bits, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+    mark_blocks<long long>(a, a.bits, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
 // The bitmap of blocks in use, as the planning CTA has it: marked before, or
@@ -84,7 +86,7 @@ __device__ unsigned *marked_bits(const PageArgs &a, unsigned *sh) {
     if (!a.small) return a.bits;
     for (int i = threadIdx.x; i < a.words; i += PL_NT) sh[i] = 0u;
     __syncthreads();
-    mark_blocks(a, sh, threadIdx.x, PL_NT);
+    mark_blocks<unsigned>(a, sh, threadIdx.x, PL_NT);
     __syncthreads();
     return sh;
 }
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
     pdl_wait();
     extern __shared__ unsigned map[];
     __shared__ int sh[72];
-    __shared__ int s_act[SMALL_ROWS], s_first[SMALL_ROWS], s_list[SMALL_ROWS];
+    __shared__ int s_act[SMALL_ROWS], s_first[SMALL_ROWS], s_list[SMALL_ROWS], s_len[SMALL_ROWS];
     const bool few = a.B <= SMALL_ROWS;
     int *act = few ? s_act : a.act, *first = few ? s_first : a.first, *list = few ? s_list : a.list;
     for (int b = threadIdx.x; b < a.B; b += PL_NT) {
@@ -150,7 +152,10 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
             p = a.in_place ? b : -1;
         }
         act[b] = p;
-        if (few) a.act[b] = p;
+        if (few) {
+            a.act[b] = p;
+            s_len[b] = seq_len_of(a.lens_in, b, a.P, a.max_pages, nullptr);
+        }
         first[b] = 0x7fffffff;
     }
     const unsigned *bits = marked_bits(a, map);
@@ -161,19 +166,16 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
         if (p >= 0) atomicMin(&first[p], p == b ? -1 : b);
     }
     __syncthreads();
-    auto needs = [&](int b, int &src) {
+    auto length = [&](int p) { return few ? s_len[p] : seq_len_of(a.lens_in, p, a.P, a.max_pages, nullptr); };
+    auto needs = [&](int b) {
         if (b >= a.B) return 0;
         const int p = act[b];
-        if (p < 0) return 0;
-        const int L = seq_len_of(a.lens_in, p, a.P, a.max_pages, nullptr);
-        if (L % a.P == 0 || first[p] == (p == b ? -1 : b)) return 0;
-        src = a.table_in[(size_t)p * a.max_pages + L / a.P];
-        return 1;
+        return p >= 0 && length(p) % a.P != 0 && first[p] != (p == b ? -1 : b) ? 1 : 0;
     };
     long long want = 0;
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
-        int src, tot;
-        block_excl_scan(needs(b0 + threadIdx.x, src), sh, &tot);
+        int tot;
+        block_excl_scan(needs(b0 + threadIdx.x), sh, &tot);
         want += tot;
     }
     const int have = list_free(a, bits, want < a.num_blocks ? want : a.num_blocks, list, sh);
@@ -181,7 +183,8 @@ __global__ void __launch_bounds__(PL_NT) plan_fork_kernel(const __grid_constant_
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
         const int b = b0 + threadIdx.x;
         int src = -1, tot, n_pairs;
-        const int need = needs(b, src);
+        const int need = needs(b);
+        if (need) src = __ldg(a.table_in + (size_t)act[b] * a.max_pages + length(act[b]) / a.P);
         const int at = rank + block_excl_scan(need, sh, &tot);
         rank += tot;
         int blk = -2;
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant_
     extern __shared__ unsigned map[];
     __shared__ int sh[72];
     __shared__ long long s_sum[PL_NT / 32];
-    const unsigned *bits = marked_bits(a, map);
+    __shared__ int s_list[SMALL_ROWS];
     const long long cap = (long long)a.max_pages * a.P;
     // pages sequence b needs, its pages and new length; -1: it does not grow
     auto need = [&](int b, int &n0, long long &L) {
@@ -241,28 +244,34 @@ __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant_
         }
         return x;
     };
-    long long want = 0, tot;
-    for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
-        int n0;
-        long long L;
-        scan64(max(0, need(b0 + threadIdx.x, n0, L)), tot);
+    long long want = 0, tot, L = 0, end = 0;
+    int n0 = 0, k = need(threadIdx.x, n0, L);  // of the first rows, which mostly are all
+    const unsigned *bits = marked_bits(a, map);
+    end = scan64(max(0, k), tot);
+    want = tot;
+    const long long first = tot;
+    for (int b0 = PL_NT; b0 < a.B; b0 += PL_NT) {
+        int n;
+        long long l;
+        scan64(max(0, need(b0 + threadIdx.x, n, l)), tot);
         want += tot;
     }
-    const int have = list_free(a, bits, want < a.num_blocks ? want : a.num_blocks, a.list, sh);
-    long long used = 0;
+    int *list = want <= SMALL_ROWS ? s_list : a.list;
+    const int have = list_free(a, bits, want < a.num_blocks ? want : a.num_blocks, list, sh);
+    long long used = first;
     for (int b0 = 0; b0 < a.B; b0 += PL_NT) {
         const int b = b0 + threadIdx.x;
-        int n0 = 0;
-        long long L = 0;
-        const int k = need(b, n0, L);
-        const long long end = used + scan64(max(0, k), tot);
-        used += tot;
+        if (b0) {
+            k = need(b, n0, L);
+            end = used + scan64(max(0, k), tot);
+            used += tot;
+        }
         if (k < 0) continue;
         if (end > have && k > 0) {
             atomicOr(a.status, ENTMAXKV_STATUS_NO_BLOCK);
             continue;
         }
-        for (int i = 0; i < k; ++i) a.table_out[(size_t)b * a.max_pages + n0 + i] = a.list[end - k + i];
+        for (int i = 0; i < k; ++i) a.table_out[(size_t)b * a.max_pages + n0 + i] = list[end - k + i];
         a.lens_out[b] = (int)L;
     }
 }
@@ -498,7 +507,7 @@ int on_device(PageArgs *a) {
     return rc;
 }
 
-constexpr int GRID = 148 * 8;
+constexpr int GRID = 148 * 16;  // two or more rounds of CTAs even the rows and chunks out (148 * 8: 4% slower)
 
 // The planning launch, after the marking ones where the table is large.
 template <class K>

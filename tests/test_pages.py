@@ -293,6 +293,41 @@ def test_grow(B, hold):
 
 
 @gpu
+@pytest.mark.parametrize("B,mp,nb", [(3, 5, 7168 * 32), (3, 5, 7168 * 32 + 1), (4, 16384, 70000), (4, 16385, 70000),
+                                     (1024, 3, 5000), (1025, 3, 5000)])
+def test_where_the_plan_moves_off_the_chip(B, mp, nb):
+    """Pools and tables around the sizes up to which one CTA marks the blocks and keeps the rows by itself."""
+    P = 16
+    rng = np.random.RandomState(nb)
+    lens = rng.randint(0, min(mp, 40) * P, B)
+    p = Pool(B, P, mp, nb, lens, seed=1, words=4, bufs=1)
+    parent = rng.randint(-1, B, B)
+    want_t, want_l, pairs, short = ref.fork(parent, p.table, p.lens, P, nb)
+    want = p.host_data()
+    for s, d in pairs:
+        want[:, d] = want[:, s]
+    t_out, l_out = torch.full((B, mp), 77, dtype=torch.int32, device="cuda"), i32([77] * B)
+    pages.entmaxkv_pages_fork(p.shape, i32(parent), i32(p.table), i32(p.lens), t_out, l_out, p.buffers, workspace=p.ws)
+    assert not short and nv.get_status() == 0
+    np.testing.assert_array_equal(t_out.cpu().numpy(), want_t)
+    np.testing.assert_array_equal(l_out.cpu().numpy(), want_l)
+    add = rng.randint(0, 3, B)
+    want_t, want_l, short = ref.grow(add, want_t, want_l, P, nb)
+    pages.entmaxkv_pages_grow(p.shape, i32(add), t_out, l_out, workspace=p.ws)
+    np.testing.assert_array_equal(t_out.cpu().numpy(), want_t)
+    np.testing.assert_array_equal(l_out.cpu().numpy(), want_l)
+    want_t, remap, live, pairs = ref.compact(want_t, want_l, P, nb)
+    for s, d in pairs:
+        want[:, d] = want[:, s]
+    r_out, n_live = i32([-7] * nb), i32([-7])
+    pages.entmaxkv_pages_compact(p.shape, t_out, l_out, t_out, p.buffers, r_out, n_live, workspace=p.ws)
+    assert int(n_live) == live and nv.get_status(clear=True) in (0, nv.STATUS_BAD_LENGTH)
+    np.testing.assert_array_equal(r_out.cpu().numpy(), remap)
+    np.testing.assert_array_equal(t_out.cpu().numpy(), want_t)
+    np.testing.assert_array_equal(p.host_data(), want)
+
+
+@gpu
 def test_grow_without_enough_blocks():
     """Needs are counted in order, those that fail too; a row that needs no block grows all the same."""
     p = Pool(5, 16, 6, 10, [16, 16, 10, 0, 16], share=False)
