@@ -13,7 +13,7 @@
  * long.  Every (token, kv head, 64 consecutive coordinates) is quantised by
  * itself, every fl() a rounding to fp32:
  *   lo   = min x                           (a bf16 value)
- *   s    = bf16(fl(fl(max x - lo) / 15)),  0 when below 2^-126
+ *   s    = bf16(fl(fl(max x - lo) * fl(1/15))),  0 when below 2^-126
  *   code = clamp(rint(fl(fl(x - lo) * fl(1 / s))), 0, 15),  0 when s = 0
  * and stands for  value = fl(s * code + lo),  so |value - x| is at most half a
  * step s plus rounding.  A group that holds a NaN or an infinity, or whose
@@ -101,7 +101,10 @@ ENTMAXKV_API size_t entmaxkv_kv4_workspace_size(const entmaxkv_shape *shape);
  *               read; tau_out (nullable) gets tau
  *   alpha == 1: out = sum_T softmax(s)_t v_t; tau_out gets log sum_T exp(s_t)
  * with k_t, v_t the values the codes stand for.  out fp32 [B][Hq][d] (may be
- * pinned host memory), tau_out fp32 [B][Hq].  A head without tokens gets
+ * pinned host memory), tau_out fp32 [B][Hq].  Scores are held in fp32 in the
+ * units of a query whose largest coordinate is near 2^13, softmax weights in
+ * units of the values' steps: beyond magnitudes of 2^100, keys may overflow
+ * and values lose their smallest weights.  A head without tokens gets
  * out = 0, tau = NaN; a non-finite query row NaN, and
  * ENTMAXKV_STATUS_NONFINITE.  NaN values that carry weight, and NaN keys,
  * make out NaN.  Results do not depend on the order in which CTAs run.

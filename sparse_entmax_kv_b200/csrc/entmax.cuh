@@ -86,4 +86,28 @@ __device__ float entmax_tau(ForEach for_each, int n, float lo, float hi, float z
     return t;
 }
 
+// The same root by halving [lo, hi], for any r > 0.  With r < 1 a token that
+// comes into the support does so with an infinite slope, and Newton's steps
+// may pass the root back and forth.
+template <int NT, class ForEach>
+__device__ float entmax_tau_halving(ForEach for_each, float lo, float hi, float r, int ri, float (*red)[NT / 32][2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int it = 0; it < 40; ++it) {
+        const float mid = 0.5f * (lo + hi);
+        if (!(mid > lo && mid < hi)) break;  // neighbours
+        float s = 0.f;
+        for_each([&](float z) { s += pos_pow(z - mid, r, ri); }, (int)threadIdx.x, NT);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+        if (lane == 0) red[it & 1][warp][0] = s;
+        __syncthreads();
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) s += red[it & 1][w][0];
+        if (s >= 1.f) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 }  // namespace ekv

@@ -55,7 +55,9 @@ constexpr int AT_MAX_WARPS = 148 * 5 * AT_WARPS;
 constexpr int AT_MIN_CHUNKS = 2;        // chunks a warp gets at least ...
 constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
 constexpr float AT_MAX_X = 32768.f;     // p s stays below this (fp16 ends at 65504) ...
-constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a reference is set
+constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a reference is set;
+constexpr float AT_MAX_Y = 0x1p115f;    // so for p |lo + 8 s|, which matters where steps are far below the values
+constexpr int AT_TOP_Y = 100;
 
 // CTAs an SM holds (registers bound the softmax, shared memory allows five).
 template <int D, int G>
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
                             y[g][e] = fmaf(p[e], P.o[0][g], p[2 + e] * P.o[1][g]);
                             // pages that the head did not select may hold anything
                             if (masked.value && !keeps<G>(mask, 2 * c + e)) x[g][e] = x[g][2 + e] = y[g][e] = 0.f;
-                            sum += x[g][e] + x[g][2 + e];
+                            sum = fmaf(fabsf(y[g][e]), AT_MAX_X / AT_MAX_Y, sum + (x[g][e] + x[g][2 + e]));
                         }
                     }
                     return sum;
@@ -638,14 +640,22 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
                         float zm = fmaxf(z[e], z[2 + e]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) zm = fmaxf(zm, __shfl_xor_sync(FULL, zm, o));
-                        float xm = 0.f;
+                        float xm = 0.f, ym = 0.f;
+                        const float p0 = exp2f(z[e] - zm), p1 = exp2f(z[2 + e] - zm);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            xm = fmaxf(xm, fmaxf(exp2f(z[e] - zm) * P.s[0][g], exp2f(z[2 + e] - zm) * P.s[1][g]));
+                        for (int g = 0; g < NG; ++g) {
+                            xm = fmaxf(xm, fmaxf(p0 * P.s[0][g], p1 * P.s[1][g]));
+                            ym = fmaxf(ym, fmaxf(p0 * fabsf(P.o[0][g]), p1 * fabsf(P.o[1][g])));
+                        }
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(FULL, xm, o));
-                        const int up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);  // xm < 2^(exponent + 1)
-                        const float nr = fmaxf(ref[e], zm - (float)max(-100, min(up, 60)));
+                        for (int o = 4; o < 32; o <<= 1) {
+                            xm = fmaxf(xm, __shfl_xor_sync(FULL, xm, o));
+                            ym = fmaxf(ym, __shfl_xor_sync(FULL, ym, o));
+                        }
+                        // below 2^(exponent + 1)
+                        const int x_up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);
+                        const int y_up = AT_TOP_Y - ((int)(__float_as_uint(ym) >> 23) - 126);
+                        const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), 100)));
                         corr[e] = exp2f(ref[e] - nr);
                         ref[e] = nr;
                         l[e] *= corr[e];
@@ -811,7 +821,7 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     __syncthreads();
     const float nan = __int_as_float(0x7fc00000);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
-    // den is 0 only without tokens (a share with tokens has a weight of 2^-100
+    // den is 0 only without tokens (a share with tokens has a weight of 2^-120
     // at least); NaN scores make it NaN
     const bool none = den == 0.f;
     if (sub == 0) {
@@ -1208,12 +1218,13 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const float hi = zmax - powf((float)nc, 1.f - a.alpha);
     float tau = thr;
     if (nc > 1 && hi > thr) {
-        if (onchip)
-            tau = entmax_tau<TK_NT>([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); }, nc,
-                                    thr, hi, zmax, r, ri, red);
-        else  // every thread adds the candidates of its place, pass by pass
-            tau = entmax_tau<TK_NT>([&](auto add, int, int) { each([&](int, float z, int) { add(z); }); }, nc, thr, hi,
-                                    zmax, r, ri, red);
+        // off chip every thread adds the candidates of its place, pass by pass
+        auto solve = [&](auto for_each) {
+            return r >= 1.f ? entmax_tau<TK_NT>(for_each, nc, thr, hi, zmax, r, ri, red)
+                            : entmax_tau_halving<TK_NT>(for_each, thr, hi, r, ri, red);
+        };
+        if (onchip) tau = solve([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); });
+        else tau = solve([&](auto add, int, int) { each([&](int, float z, int) { add(z); }); });
     }
     if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = tau;
 

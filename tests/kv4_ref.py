@@ -23,7 +23,7 @@ def quantise(x):
         lo, hi = g.min(-1), g.max(-1)
         rng = f32(hi - lo)
         bad = ~np.isfinite(g).all(-1) | ~np.isfinite(rng)
-        s = np.where(bad, 0, bf16(f32(np.where(bad, 0, rng) / 15)))
+        s = np.where(bad, 0, bf16(f32(np.where(bad, 0, rng) * f32(1 / 15))))
         s = np.where(s < 2.0 ** -126, 0, s)
         inv = np.where(s > 0, f32(1 / np.where(s > 0, s, 1)), 0)
         c = np.clip(np.rint(f32(f32(g - np.where(bad, 0, lo)[..., None]) * inv[..., None])), 0, 15)

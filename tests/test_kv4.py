@@ -339,6 +339,68 @@ def test_decode_kept_pages(alpha, G, Hkv, d, P):
 
 
 @gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("ks,vs,qs", [(1e-20, 1.0, 1e20), (1e20, 1.0, 1e-20), (1.0, 1e30, 1.0), (1.0, 1e-25, 1.0),
+                                      (1e-30, 1e-30, 1.0), (4.0, 1.0, 8.0)])
+def test_scales(alpha, ks, vs, qs):
+    """Keys, values and queries of any magnitude; the last case has scores far apart (one token takes nearly all)."""
+    def rows(k, v):
+        v *= vs
+    c = Case(2, 4, 2, 128, 32, [700, 33], seed=9, scale=ks, rows=rows)
+    c.q = (c.q.float() * qs).bfloat16()
+    c.write(meta=False)
+    out, tau = c.decode(alpha)
+    c.check_decode(alpha, out, tau)
+    assert nv.get_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.05, 1.1, 3.0, 10.0])
+def test_unusual_alphas(alpha):
+    c = Case(2, 2, 1, 64, 16, [2000, 50], seed=4)
+    c.write(meta=False)
+    out, tau = c.decode(alpha)
+    c.check_decode(alpha, out, tau)
+
+
+@gpu
+def test_values_that_grow_along_the_sequence():
+    """The reference of the softmax has to follow p s wherever it rises: steps 2^60 apart, scores 40 apart."""
+    def rows(k, v):
+        n = k.shape[0]
+        v *= 2.0 ** torch.linspace(-30, 30, n)[:, None, None]
+        k *= torch.linspace(0, 6, n)[:, None, None]
+    c = Case(1, 4, 1, 64, 16, [900], seed=6, rows=rows)
+    c.write(meta=False)
+    c.check_decode(1.0, *c.decode(1.0))
+
+
+@gpu
+def test_constant_values():
+    """Groups without a step (s = 0): only the offsets count, however large they are and wherever they appear."""
+    def rows(k, v):
+        v[:] = torch.arange(v.shape[0])[:, None, None] % 7 - 3.0
+        v[200] = 1e30
+        v[300] = -1e35
+    c = Case(1, 4, 1, 64, 16, [500], seed=7, rows=rows)
+    c.write(meta=False)
+    c.check_decode(1.0, *c.decode(1.0))
+    c.check_decode(1.5, *c.decode(1.5))
+
+
+@gpu
+@pytest.mark.parametrize("alpha,scale", [(1.25, 1.0), (1.25, 0.2), (1.5, 0.1)])
+def test_more_candidates_than_fit_on_chip(alpha, scale):
+    """Thousands of tokens above max z - 1: the histogram's cut, and supports beyond it."""
+    c = Case(2, 2, 1, 64, 32, [40000, 12345], seed=8, scale=scale)
+    c.write(meta=False)
+    out, tau = c.decode(alpha)
+    c.check_decode(alpha, out, tau)
+    again = c.decode(alpha)
+    assert torch.equal(out, again[0]) and torch.equal(tau, again[1])
+
+
+@gpu
 @pytest.mark.parametrize("alpha", [1.5, 2.0])
 def test_large_supports(alpha):
     """All scores nearly equal: every token carries weight, far more than the threshold kernel holds on chip."""
