@@ -444,7 +444,8 @@ def oracle_step_sample(wl, inp_host, seconds_target=10.0, max_reps=3):
 
     policy = wl.policy if wl.policy != "dense" else "topk"
     h = inp_host
-    meta = orc.build_meta(h["K"], h["page_table"], h["seq_lens"], wl.Hkv, wl.d, wl.P, wl.num_blocks)
+    # records by physical block: a sequence of a batch may lie anywhere in the pool
+    meta = orc.build_meta(h["K"], h["page_table"], h["seq_lens"], wl.Hkv, wl.d, wl.P, h["K"].shape[0])
     times = []
     t_end = time.perf_counter() + seconds_target
     for _ in range(max_reps):
