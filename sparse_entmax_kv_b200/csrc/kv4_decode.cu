@@ -768,10 +768,8 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
     }
 }
 
-constexpr int CB_NT = 256;
-
 // The shares of a head, merged in token order.
-template <int D>
+template <int D, int CB_NT>
 __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int SUB = CB_NT / D;
@@ -1368,7 +1366,10 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
         share_out(a, sms, softmax_ctas<D, G>());
         e = run_shares(kv4_softmax_kernel<D, G>, a, AT_WARPS * TileRing<D, true>::BYTES, st);
         if (e != cudaSuccess) return e;
-        return launch_pdl(kv4_combine_kernel<D>, dim3(heads), dim3(CB_NT), (size_t)a.W * 4, st, a);
+        // few heads have many shares each: more threads for one
+        const bool few = heads <= sms;
+        return launch_pdl(few ? kv4_combine_kernel<D, 1024> : kv4_combine_kernel<D, 256>, dim3(heads),
+                          dim3(few ? 1024 : 256), (size_t)a.W * 4, st, a);
     }
     share_out(a, sms, SCAN_CTAS);
     // short shares list little that a common max would have cut: no launch to reset it
