@@ -19,7 +19,7 @@
 //           and sum_t p_t (lo_tg + 8 s_tg) is added at the end.  The
 //           reference of a head's softmax is placed so that its largest p s
 //           lies between 2^9 and 2^15: what is lost of a weight is below 2^-34
-//           of the largest.  Groups of four heads or fewer put the two parts
+//           of the largest (values below 2^-90 get less).  Groups of four heads or fewer put the two parts
 //           in the columns their heads leave free.  The sums move to a second
 //           set of fp32 registers every few tiles, so that few truncations
 //           meet a large sum.
@@ -38,6 +38,19 @@
 //            row) for each warp and group; tau_kernel, one CTA a head, drops
 //            those below the head's max - 1, solves for tau and sums p v over
 //            the support
+//
+// What bounds it: instructions, then memory.  A 16-token tile of 128
+// coordinates (2304 bytes with its values) takes about 420 warp instructions
+// with its values and 260 without, most of them to make operands of codes; the
+// integer pipe is 50 to 55 % busy, the issue slots 60 to 65 %, the tensor
+// pipe 15 %.  Softmax over 8 sequences of 16k to 32k tokens, 8 kv heads of 4,
+// d = 128: 71 us, 236 MB at 3.3 TB/s (50 % of a copy's rate); entmax over 4
+// of 64k to 128k: 122 us, of which the scan is 105 (271 MB at 2.6 TB/s).
+// Tried and dropped: units of a quarter of a warp's share, taken from a queue
+// in one CTA an SM (71 -> 84 us, 126 -> 145: each pays for its queries and its
+// first copies again); key codes uncentred, straight from the mask (4 to 6 %
+// faster, entmax 2.5 times as far off); the shift of a code word on the
+// multiplier (71 -> 77 us); four stages to a ring (no gain).
 #include <cmath>
 #include <cstring>
 
@@ -123,7 +136,7 @@ struct Share {
 // itself: lane i sums entries i C .. i C + C - 1.  The lists of selections are
 // about alike in length and may be many: there each group's list is cut in
 // a.S shares, and no warp has to know the other groups' (16 x 32 lists of 32
-// pages: 28 us for the scan with the range, see the table of times).
+// pages: the scan 28 us with the range, 18 so).
 struct Walk {
     int w;             // the warp, or its next share
     long long t, end;  // chunks [t, end) of the range are left
@@ -916,7 +929,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         // The first tiles of a share are tested together, against the largest
         // score that the warps of the head have met in theirs (alone, a warp
         // lists nearly all of them, and the tau kernel has to drop them again:
-        // entmax over 4 x 128k tokens 206 us without, see the table of times).
+        // entmax over 4 x 128k tokens took 206 us so, and 163 with it).
         auto settle = [&] {
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
@@ -1366,8 +1379,10 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
         share_out(a, sms, softmax_ctas<D, G>());
         e = run_shares(kv4_softmax_kernel<D, G>, a, AT_WARPS * TileRing<D, true>::BYTES, st);
         if (e != cudaSuccess) return e;
-        // few heads have many shares each: more threads for one
-        const bool few = heads <= sms;
+        // heads of many shares get more threads while every SM has a place for
+        // one (24 heads of 512 shares: 31 us in all with 1024 threads, 49 with
+        // 256; 8 heads of 22 shares: 12.6 and 10.6)
+        const bool few = heads <= sms && (long long)a.W > 64ll * a.B * a.nk;
         return launch_pdl(few ? kv4_combine_kernel<D, 1024> : kv4_combine_kernel<D, 256>, dim3(heads),
                           dim3(few ? 1024 : 256), (size_t)a.W * 4, st, a);
     }

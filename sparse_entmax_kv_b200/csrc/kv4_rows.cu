@@ -12,6 +12,13 @@
 // metadata the page's key tiles are also kept in shared memory, old tokens
 // copied in, and 1024 / d threads share the statistics of a coordinate.
 // read: the same split, the other way round.
+//
+// 38.5k rows of 8 heads, d = 128, pages of 64 (12 prompts of 2k to 4k tokens):
+// write 51 us without metadata and 79 with it (210 MB: 32 at a copy's rate),
+// read 43.  Bound by instructions: the integer pipe is half busy, issue 70 %;
+// the statistics are 28 us of the write, 8 of them conversions to fp64.  One
+// appended token a sequence (32 x 8 heads) takes 9.5 us cold: three dependent
+// loads, the page's old tiles, 64 tokens of statistics.
 #include <cmath>
 
 #include "../../include/entmaxkv_kv4.h"

@@ -615,6 +615,44 @@ def test_pinned_rows_and_output():
 
 
 @gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_blocks_beyond_four_gigabytes(alpha):
+    """Blocks at the far end of caches of 4.8 GB each."""
+    nb = 130000
+    shape = nv.Shape(1, 16, 8, 128, 64, 3, nb)
+    assert kv4.bytes_of(shape) > 1 << 32
+    k4, v4 = kv4.alloc_cache(shape, "cuda")
+    c = Case(1, 16, 8, 128, 64, [150], seed=2)
+    c.shape, c.k4, c.v4, c.mp = shape, k4, v4, 3
+    c.table = torch.tensor([[nb - 1, 116600, nb - 2]], dtype=torch.int32, device="cuda")
+    c.ws = kv4.alloc_workspace(shape, "cuda")
+    c.write(meta=False)
+    c.check_decode(alpha, *c.decode(alpha))
+    back = [torch.empty(150, 8, 128, device="cuda") for _ in range(2)]
+    kv4.entmaxkv_kv4_read(shape, k4, v4, c.start, c.table, c.seq, *back)
+    for x, b in ((c.k, back[0]), (c.v, back[1])):
+        assert torch.equal(b.cpu(), torch.from_numpy(ref.values(*ref.quantise(f64_of(x)))).float())
+    assert nv.get_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_a_stream_that_is_given(alpha):
+    """Calls go to the stream they are given, not to the current one."""
+    c = Case(2, 8, 2, 64, 16, [500, 90])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    big = torch.empty(1 << 26, device="cuda")
+    with torch.cuda.stream(side):
+        big.fill_(1.0)  # keeps the side stream busy while the current one runs ahead
+    kv4.entmaxkv_kv4_write(c.shape, c.k, c.v, c.start, c.table, c.seq, c.k4, c.v4, c.meta, stream=side)
+    out, tau = torch.empty(2, 8, 64, device="cuda"), torch.empty(2, 8, device="cuda")
+    kv4.entmaxkv_kv4_decode(c.shape, c.q, c.k4, c.v4, c.table, c.seq, alpha, out, tau, workspace=c.ws, stream=side)
+    side.synchronize()
+    c.check_decode(alpha, out, tau)
+
+
+@gpu
 def test_binding_refusals_on_the_gpu():
     c = Case(2, 4, 2, 64, 16, [10, 20])
     with pytest.raises(ValueError, match="packed"):

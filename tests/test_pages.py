@@ -380,6 +380,20 @@ def test_copy(nb, words, n, bufs):
 
 
 @gpu
+def test_copy_beyond_four_gigabytes():
+    """Blocks at the far end of a 5 GB buffer, and blocks that end inside a chunk."""
+    words, nb = 32768 + 4, 38000
+    a = torch.empty(nb, words, dtype=torch.int32, device="cuda")
+    a[nb - 1].copy_(torch.arange(words, dtype=torch.int32))
+    a[nb - 2].fill_(7)
+    b = torch.zeros(2, words, dtype=torch.int32, device="cuda")
+    pages.entmaxkv_pages_copy(pages.Buffers([a]), pages.Buffers([b]), i32([nb - 1, nb - 2]), i32([1, 0]))
+    assert torch.equal(b[1].cpu(), torch.arange(words, dtype=torch.int32)) and (b[0] == 7).all()
+    pages.entmaxkv_pages_copy(pages.Buffers([b]), pages.Buffers([a]), i32([1]), i32([nb - 3]))
+    assert torch.equal(a[nb - 3], b[1])
+
+
+@gpu
 def test_copy_to_pinned_memory_and_bad_ids():
     a = torch.randint(-9, 9, (2, 8, 64), dtype=torch.int32).cuda()
     host = torch.zeros(2, 4, 64, dtype=torch.int32).pin_memory()
