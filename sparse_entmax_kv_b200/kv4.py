@@ -75,6 +75,16 @@ def arg(t, dtype, shape, name, device, pinned_ok=False):
     return p
 
 
+def room(workspace, device):
+    """Address of a workspace."""
+    if isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.get_device() == device \
+            and workspace.is_contiguous():
+        return workspace.data_ptr()
+    p = nv._ptr(workspace, torch.uint8, "workspace")
+    on_current_device(workspace)
+    return p
+
+
 def bytes_of(shape: nv.Shape) -> int:
     """Bytes of one 4-bit cache (keys or values)."""
     return lib().entmaxkv_kv4_bytes(C.byref(shape))
@@ -132,18 +142,31 @@ def _rows(shape, x, name, dtypes, pinned_ok):
 
 
 def _row_pair(shape, k, v, names, dtypes, row_start, stream, pinned_ok=False):
-    pk, sk = _rows(shape, k, names[0], dtypes, pinned_ok)
-    pv, sv = _rows(shape, v, names[1], dtypes, pinned_ok)
-    n = k.shape[0]
-    if n != v.shape[0] or sk != sv or k.dtype != v.dtype:
-        raise ValueError(f"{names[0]} and {names[1]}: expected the same rows, strides and dtype")
-    device, stream = current(stream)
-    for x in (k, v):
-        if x.is_cuda and x.get_device() != device:
-            on_current_device(x)
-    if row_start is None and n != shape.B:
-        raise ValueError(f"{names[0]}: one row a sequence ({shape.B}) without row_start, got {n}")
-    return pk, pv, sk, arg(row_start, torch.int32, (shape.B + 1,), "row_start", device), n, device, stream
+    """Addresses of the key and value rows and their stride, of row_start, the number of rows, device and stream."""
+    Hkv, d = shape.Hkv, shape.d
+    n = -1
+    if isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.is_cuda:
+        device, st = current(stream)
+        form, steps = k.shape, k.stride()
+        if len(form) == 3 and form[1] == Hkv and form[2] == d and steps[2] == 1 and (steps[1] == d or Hkv == 1) \
+                and k.dtype in dtypes and v.dtype == k.dtype and v.shape == form and v.stride() == steps \
+                and k.get_device() == device and v.get_device() == device:
+            n, stride, pk, pv = form[0], steps[0], k.data_ptr(), v.data_ptr()
+            if n <= 1:
+                stride = Hkv * d
+    if n < 0:  # pinned rows, or something to refuse
+        pk, stride = _rows(shape, k, names[0], dtypes, pinned_ok)
+        pv, other = _rows(shape, v, names[1], dtypes, pinned_ok)
+        n = k.shape[0]
+        if n != v.shape[0] or stride != other or k.dtype != v.dtype:
+            raise ValueError(f"{names[0]} and {names[1]}: expected the same rows, strides and dtype")
+        device, st = current(stream)
+        on_current_device(k, v)
+    if row_start is None:
+        if n != shape.B:
+            raise ValueError(f"{names[0]}: one row a sequence ({shape.B}) without row_start, got {n}")
+        return pk, pv, stride, None, n, device, st
+    return pk, pv, stride, arg(row_start, torch.int32, (shape.B + 1,), "row_start", device), n, device, st
 
 
 def entmaxkv_kv4_write(shape, k_new, v_new, row_start, page_table, seq_lens, k4, v4, meta=None, stream=None):
@@ -153,16 +176,18 @@ def entmaxkv_kv4_write(shape, k_new, v_new, row_start, page_table, seq_lens, k4,
                                                   stream, True)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
     m = None if meta is None else arg(meta, torch.uint8, (_meta_bytes(shape),), "meta", device)
-    nv._check("entmaxkv_kv4_write", lib().entmaxkv_kv4_write(
-        C.byref(shape), pk, pv, stride, ps, n, pt, sl, c4k, c4v, m, st))
+    rc = lib().entmaxkv_kv4_write(C.byref(shape), pk, pv, stride, ps, n, pt, sl, c4k, c4v, m, st)
+    if rc:
+        nv._check("entmaxkv_kv4_write", rc)
 
 
 def entmaxkv_kv4_read(shape, k4, v4, row_start, page_table, seq_lens, k_out, v_out, stream=None):
     """The last tokens of every sequence into rows [n, Hkv, d], bf16 or fp32: the inverse of entmaxkv_kv4_write."""
     pk, pv, stride, ps, n, device, st = _row_pair(shape, k_out, v_out, ("k_out", "v_out"), _ROWS, row_start, stream)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
-    nv._check("entmaxkv_kv4_read", lib().entmaxkv_kv4_read(
-        C.byref(shape), c4k, c4v, stride, ps, n, pt, sl, _ROWS[k_out.dtype], pk, pv, st))
+    rc = lib().entmaxkv_kv4_read(C.byref(shape), c4k, c4v, stride, ps, n, pt, sl, _ROWS[k_out.dtype], pk, pv, st)
+    if rc:
+        nv._check("entmaxkv_kv4_read", rc)
 
 
 def entmaxkv_kv4_decode(shape, q, k4, v4, page_table, seq_lens, alpha, out, tau_out=None, sel=None, cnt=None, *,
@@ -170,14 +195,17 @@ def entmaxkv_kv4_decode(shape, q, k4, v4, page_table, seq_lens, alpha, out, tau_
     """Attention of q (bf16 [B, Hq, d]) over the 4-bit cache into out (fp32 [B, Hq, d]): softmax (alpha = 1) or
     alpha-entmax, over the selected pages, or over all of them without sel and cnt."""
     device, st = current(stream)
-    heads = (shape.B, shape.Hq)
-    rows = heads + (shape.d,)
+    B, Hq = shape.B, shape.Hq
+    heads, rows = (B, Hq), (B, Hq, shape.d)
     c4k, c4v, pt, sl = _cache_args(shape, k4, v4, page_table, seq_lens, device)
-    ws = nv._ptr(workspace, torch.uint8, "workspace")
-    if workspace.get_device() != device:
-        on_current_device(workspace)
-    nv._check("entmaxkv_kv4_decode", lib().entmaxkv_kv4_decode(
-        C.byref(shape), arg(q, torch.bfloat16, rows, "q", device), c4k, c4v, pt, sl,
-        arg(sel, torch.int32, heads + (shape.max_pages,), "sel", device), arg(cnt, torch.int32, heads, "cnt", device),
-        float(alpha), arg(out, torch.float32, rows, "out", device, pinned_ok=True),
-        arg(tau_out, torch.float32, heads, "tau_out", device), ws, workspace.numel(), st))
+    ps = pc = None
+    if sel is not None:
+        ps = arg(sel, torch.int32, (B, Hq, shape.max_pages), "sel", device)
+    if cnt is not None:
+        pc = arg(cnt, torch.int32, heads, "cnt", device)
+    rc = lib().entmaxkv_kv4_decode(
+        C.byref(shape), arg(q, torch.bfloat16, rows, "q", device), c4k, c4v, pt, sl, ps, pc, float(alpha),
+        arg(out, torch.float32, rows, "out", device, True), arg(tau_out, torch.float32, heads, "tau_out", device),
+        room(workspace, device), workspace.numel(), st)
+    if rc:
+        nv._check("entmaxkv_kv4_decode", rc)

@@ -12,7 +12,7 @@ import ctypes as C
 import torch
 
 from . import native as nv
-from .kv4 import arg, current, on_current_device
+from .kv4 import arg, current, on_current_device, room
 
 EXPORTED = ("entmaxkv_pages_workspace_size", "entmaxkv_pages_refs", "entmaxkv_pages_fork", "entmaxkv_pages_grow",
             "entmaxkv_pages_compact", "entmaxkv_pages_copy")
@@ -114,13 +114,6 @@ def _metas(b, shape, name, device):
     return b.ref
 
 
-def _ws(workspace, device):
-    p = nv._ptr(workspace, torch.uint8, "workspace")
-    if workspace.get_device() != device:
-        on_current_device(workspace)
-    return p, workspace.numel()
-
-
 def entmaxkv_pages_refs(shape, page_table, seq_lens, refs=None, n_free=None, hold=None, *, workspace, stream=None):
     """refs (int32 [num_blocks]): rows that reach each block, plus holds; n_free (int32 [1]): blocks without any."""
     B, nb = shape.B, shape.num_blocks
@@ -128,7 +121,7 @@ def entmaxkv_pages_refs(shape, page_table, seq_lens, refs=None, n_free=None, hol
     nv._check("entmaxkv_pages_refs", lib().entmaxkv_pages_refs(
         C.byref(shape), _i32(page_table, (B, shape.max_pages), "page_table", dev),
         _i32(seq_lens, (B,), "seq_lens", dev), _i32(hold, (nb,), "hold", dev), _i32(refs, (nb,), "refs", dev),
-        _i32(n_free, (1,), "n_free", dev), *_ws(workspace, dev), st))
+        _i32(n_free, (1,), "n_free", dev), room(workspace, dev), workspace.numel(), st))
 
 
 def entmaxkv_pages_fork(shape, parent, table_in, lens_in, table_out, lens_out, buffers, meta_in=None, meta_out=None,
@@ -142,7 +135,7 @@ def entmaxkv_pages_fork(shape, parent, table_in, lens_in, table_out, lens_out, b
         _i32(lens_in, (B,), "lens_in", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
         _i32(table_out, table, "table_out", dev), _i32(lens_out, (B,), "lens_out", dev),
         _buffers(buffers, shape, "buffers", dev), _metas(meta_in, shape, "meta_in", dev),
-        _metas(meta_out, shape, "meta_out", dev), *_ws(workspace, dev), st))
+        _metas(meta_out, shape, "meta_out", dev), room(workspace, dev), workspace.numel(), st))
 
 
 def entmaxkv_pages_grow(shape, n_add, page_table, seq_lens, hold=None, *, workspace, stream=None):
@@ -152,7 +145,7 @@ def entmaxkv_pages_grow(shape, n_add, page_table, seq_lens, hold=None, *, worksp
     nv._check("entmaxkv_pages_grow", lib().entmaxkv_pages_grow(
         C.byref(shape), _i32(n_add, (B,), "n_add", dev), _i32(hold, (shape.num_blocks,), "hold", dev),
         _i32(page_table, (B, shape.max_pages), "page_table", dev), _i32(seq_lens, (B,), "seq_lens", dev),
-        *_ws(workspace, dev), st))
+        room(workspace, dev), workspace.numel(), st))
 
 
 def entmaxkv_pages_compact(shape, table_in, seq_lens, table_out, buffers, remap, n_live, hold=None, *, workspace,
@@ -163,7 +156,7 @@ def entmaxkv_pages_compact(shape, table_in, seq_lens, table_out, buffers, remap,
     nv._check("entmaxkv_pages_compact", lib().entmaxkv_pages_compact(
         C.byref(shape), _i32(table_in, table, "table_in", dev), _i32(seq_lens, (shape.B,), "seq_lens", dev),
         _i32(hold, nb, "hold", dev), _i32(table_out, table, "table_out", dev), _buffers(buffers, shape, "buffers", dev),
-        _i32(remap, nb, "remap", dev), _i32(n_live, (1,), "n_live", dev), *_ws(workspace, dev), st))
+        _i32(remap, nb, "remap", dev), _i32(n_live, (1,), "n_live", dev), room(workspace, dev), workspace.numel(), st))
 
 
 def entmaxkv_pages_copy(src, dst, src_ids, dst_ids, stream=None):
