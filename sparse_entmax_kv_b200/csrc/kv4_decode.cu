@@ -94,6 +94,7 @@ struct Kv4DecodeArgs {
     int W;                // warps that share the chunks at most
     int S;                // with selections: shares of a group
     int ct, lc;           // tiles of a chunk (1 or 2), log2 of the chunks of a page
+    int npg;              // pages of a ring stage
     int B, Hq, Hkv, P, max_pages, num_blocks;
     int kv0, nk;
     float alpha;
@@ -250,17 +251,21 @@ __device__ __forceinline__ GroupShares group_shares(const Kv4DecodeArgs &a, int 
 
 // --------------------------------------------------------------- the ring of tiles
 
-// A stage holds a chunk: the one or two tiles (16 or 32 tokens) of a page that
-// lie together, of the keys (and behind them of the values).
-constexpr int RING_STAGES = 3;
+// A stage holds four tiles (64 tokens): one, two or four pages of the list, of
+// the keys and behind them of the values.  Each page is copied by the lane that
+// has its entry, so a stage costs one pass of the warp whatever the page size
+// (with a stage for every 32 tokens of a page instead: softmax of 8 x 32k
+// tokens 87 us against 80 with pages of 16, 75 against 75 with 32; entmax of 4
+// x 128k tokens 154 against 135 with 16, 125 against 117 with 64).
+constexpr int RING_STAGES = 2;
 template <int D, bool BOTH>
 struct TileRing {
-    static constexpr int HALF = 2 * Kv4<D>::TILE;
+    static constexpr int HALF = 4 * Kv4<D>::TILE;
     static constexpr int STAGE = HALF * (BOTH ? 2 : 1);
     static constexpr int BYTES = RING_STAGES * STAGE;
     unsigned char *base;
     uint64_t *bar;
-    int2 *info;              // first cache row (block P + slot); valid tokens, and the head mask << 8
+    int2 (*info)[4];         // of each page: its first cache row (block P + slot); valid tokens, and the head mask << 8
     int in = 0, out = 0;     // stages to fill and to take next
     unsigned parity = 0;     // of the stage to take
     int flying = 0;          // filled, not taken
@@ -268,12 +273,12 @@ struct TileRing {
     int row = 0, tokens = 0, mask = 0;
     size_t at = 0;           // its byte offset in the cache
 
-    __device__ __forceinline__ void init(unsigned char *b, uint64_t *bars, int2 *i) {
+    __device__ __forceinline__ void init(const Kv4DecodeArgs &a, unsigned char *b, uint64_t *bars, int2 (*i)[4]) {
         base = b;
         bar = bars;
         info = i;
         if ((threadIdx.x & 31) == 0) {
-            for (int s = 0; s < RING_STAGES; ++s) mbar_init(&bar[s], 1);
+            for (int s = 0; s < RING_STAGES; ++s) mbar_init(&bar[s], a.npg);
             mbar_fence_init();
         }
         __syncwarp();
@@ -310,18 +315,24 @@ struct TileRing {
         row = (unsigned)blk * a.P;
         at = kv4_tile<D>(blk, a.Hkv, s.kvh, a.P, 0);
     }
-    // Starts the copy of a chunk of the list into the next free stage.
-    __device__ __forceinline__ void issue(const Kv4DecodeArgs &a, const Share &s, int chunk) {
-        const int e = chunk >> a.lc;
+    // Stages that a share takes.
+    __device__ __forceinline__ int stages(const Kv4DecodeArgs &a, const Share &s) const {
+        return s.last > s.first ? (((s.last - 1) >> a.lc) - (s.first >> a.lc)) / a.npg + 1 : 0;
+    }
+    // Starts the copies of stage k of a share into the next free stage.
+    __device__ __forceinline__ void issue(const Kv4DecodeArgs &a, const Share &s, int k) {
+        const int e = (s.first >> a.lc) + k * a.npg;
         if ((unsigned)(e - e0) >= 32u) window(a, s, e);
-        if ((int)(threadIdx.x & 31) == e - e0) {  // the lane that has the entry
-            const int t16 = (chunk & ((1 << a.lc) - 1)) * a.ct;
-            const int nval = max(0, min(16 * a.ct, tokens - 16 * t16));
-            info[in] = make_int2(row + 16 * t16, nval | (mask << 8));
+        const int piece = (int)(threadIdx.x & 31) - (e - e0);
+        if ((unsigned)piece < (unsigned)a.npg) {  // the lanes that have the entries
+            const int tp = a.ct << a.lc, t0 = (e + piece) * tp;  // the page's tiles; those of the share are
+            const int lo = max(0, s.first * a.ct - t0), hi = min(tp, s.last * a.ct - t0);
+            const int nval = max(0, min(16 * hi, tokens) - 16 * lo);
+            info[in][piece] = make_int2(row + 16 * lo, nval | (mask << 8));
             if (nval > 0) {
-                const unsigned bytes = a.ct * Kv4<D>::TILE;
-                const size_t o = at + t16 * Kv4<D>::TILE;
-                unsigned char *dst = base + in * STAGE;
+                const unsigned bytes = ((nval + 15) >> 4) * Kv4<D>::TILE;
+                const size_t o = at + lo * Kv4<D>::TILE;
+                unsigned char *dst = base + in * STAGE + piece * tp * Kv4<D>::TILE;
                 mbar_arrive_expect_tx(&bar[in], bytes * (BOTH ? 2 : 1));
                 bulk_g2s(dst, a.k4 + o, bytes, &bar[in]);
                 if (BOTH) bulk_g2s(dst + HALF, a.v4 + o, bytes, &bar[in]);
@@ -344,10 +355,10 @@ struct TileRing {
         }
     }
     // Waits for the next stage.  False: it did not come (the status word says so).
-    __device__ __forceinline__ bool take(const Kv4DecodeArgs &a, int2 &what, unsigned char *&tile) {
+    __device__ __forceinline__ bool take(const Kv4DecodeArgs &a, const int2 *&what, const unsigned char *&tiles) {
         const bool ok = wait(a);
         what = info[out];
-        tile = base + out * STAGE;
+        tiles = base + out * STAGE;
         pass();
         return __all_sync(FULL, ok);
     }
@@ -446,7 +457,8 @@ struct Queries {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) b[i][x] = __ldg(qw + 32 * (i >> 2) + 8 * c + 4 * ((i >> 1) & 1) + 2 * (i & 1) + x);
+            for (int x = 0; x < 2; ++x)
+                b[i][x] = __ldg(qw + 32 * (i >> 2) + 8 * c + 4 * ((i >> 1) & 1) + 2 * (i & 1) + x);
     }
     __device__ __forceinline__ void finish(float scale) {
         const int lane = threadIdx.x & 31, c = lane & 3;
@@ -524,14 +536,15 @@ __device__ __forceinline__ void tile_scores(const unsigned char *tile, const Que
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 2 * g; i < 2 * g + 2; ++i) {
-            mma_f16_16816(acc, code_f16<0>(w0[i], one), code_f16<0>(w1[i], one), code_f16<1>(w0[i], one), code_f16<1>(w1[i], one),
-                          Q.b[2 * i][0], Q.b[2 * i][1]);
-            mma_f16_16816(acc, code_f16<2>(w0[i], one), code_f16<2>(w1[i], one), code_f16<3>(w0[i], one), code_f16<3>(w1[i], one),
-                          Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
+            mma_f16_16816(acc, code_f16<0>(w0[i], one), code_f16<0>(w1[i], one), code_f16<1>(w0[i], one),
+                          code_f16<1>(w1[i], one), Q.b[2 * i][0], Q.b[2 * i][1]);
+            mma_f16_16816(acc, code_f16<2>(w0[i], one), code_f16<2>(w1[i], one), code_f16<3>(w0[i], one),
+                          code_f16<3>(w1[i], one), Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
         }
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            if ((v & 1) < NE) z[v] = fmaf(P.s[v >> 1][g], acc[v], fmaf(P.o[v >> 1][g], Q.sum[g][v & 1 & (NE - 1)], z[v]));
+            if ((v & 1) < NE)
+                z[v] = fmaf(P.s[v >> 1][g], acc[v], fmaf(P.o[v >> 1][g], Q.sum[g][v & 1 & (NE - 1)], z[v]));
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v)
@@ -561,7 +574,8 @@ struct No {
 // -------------------------------------------------------------- softmax
 
 template <int D, int G>
-__global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>()))
+    kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, G>::NE;
     constexpr int NB = G == 8 ? 2 : 1;  // products per value operand: both parts, or both in one
@@ -569,21 +583,23 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
     using Ring = TileRing<D, true>;
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
-    __shared__ int2 infos[AT_WARPS][RING_STAGES];
+    __shared__ int2 infos[AT_WARPS][RING_STAGES][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
     const unsigned one = a.one;
     const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
-    ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
+    ring.init(a, rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     Walk walk(a, w);
+    const int page_bytes = (a.ct << a.lc) * Kv4<D>::TILE;
     bool alive = true;  // no wait ran out so far
     while (walk.more(a)) {
         const Share sh = walk.next(a);
         Queries<D, G> Q;
         Q.fetch(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D);
         ring.start();
-        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
+        const int stages = alive ? ring.stages(a, sh) : 0;
+        for (int i = 0; i < RING_STAGES && i < stages; ++i) ring.issue(a, sh, i);
         Q.finish(1.4426950408889634f * rsqrtf((float)D));  // z in powers of two
 
         float acc[MT][4], tot[MT][4];
@@ -595,149 +611,153 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>())) kv4_softma
         // sums of p and of p (lo + 8 s) over the lane's tokens
         float ref[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, off[NG][2] = {};
         int until = FLUSH;
-        for (int i = sh.first; i < sh.last && alive; ++i) {
-            int2 what;
-            unsigned char *stage;
-            if (!ring.take(a, what, stage)) {
+        for (int i = 0; i < stages; ++i) {
+            const int2 *whats;
+            const unsigned char *stage;
+            if (!ring.take(a, whats, stage)) {
                 ring.drain(a);
                 alive = false;  // the shares end empty, so that what reads them finds them whole
                 break;
             }
-            const int mask = what.y >> 8;
-            int n = what.y & 0xff;
 #pragma unroll 1
-            for (const unsigned char *tile = stage; n > 0; n -= 16, tile += Kv4<D>::TILE) {
-                float z[4], p[4], x[NG][4], y[NG][2];
-                tile_scores<D, G>(tile, Q, a.one, z);
-                const unsigned char *vt = tile + Ring::HALF;
-                Params<D> P;
-                P.load(vt);
-                // weights p, the x = p s, and y, the sums of p (lo + 8 s)
-                auto weights = [&](auto masked) {
-                    float sum = 0.f;
+            for (int page = 0; page < a.npg; ++page, stage += page_bytes) {
+                const int what = whats[page].y, mask = what >> 8;
+                int n = what & 0xff;
+#pragma unroll 1
+                for (const unsigned char *tile = stage; n > 0; n -= 16, tile += Kv4<D>::TILE) {
+                    float z[4], p[4], x[NG][4], y[NG][2];
+                    tile_scores<D, G>(tile, Q, a.one, z);
+                    const unsigned char *vt = tile + Ring::HALF;
+                    Params<D> P;
+                    P.load(vt);
+                    // weights p, the x = p s, and y, the sums of p (lo + 8 s)
+                    auto weights = [&](auto masked) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int e = 0; e < NE; ++e) {
+                            p[e] = ex2(z[e] - ref[e]);
+                            p[2 + e] = ex2(z[2 + e] - ref[e]);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                x[g][e] = p[e] * P.s[0][g];
+                                x[g][2 + e] = p[2 + e] * P.s[1][g];
+                                y[g][e] = fmaf(p[e], P.o[0][g], p[2 + e] * P.o[1][g]);
+                                // pages that the head did not select may hold anything
+                                if (masked.value && !keeps<G>(mask, 2 * c + e)) x[g][e] = x[g][2 + e] = y[g][e] = 0.f;
+                                sum = fmaf(fabsf(y[g][e]), AT_MAX_X / AT_MAX_Y, sum + (x[g][e] + x[g][2 + e]));
+                            }
+                        }
+                        return sum;
+                    };
+                    float sum;
+                    const bool all = whole<G>(mask, n);
+                    if (all) {
+                        sum = weights(No{});
+                    } else {
+                        mask_scores<G>(mask, n, z);
+                        // so may rows behind the sequence
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            if (r + 8 * u >= n)
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) P.s[u][g] = P.o[u][g] = 0.f;
+                        sum = weights(Yes{});
+                    }
+                    if (__any_sync(FULL, !(sum <= AT_MAX_X))) {
+                        // the reference follows the largest p s
+                        float corr[2] = {1.f, 1.f};
+#pragma unroll
+                        for (int e = 0; e < NE; ++e) {
+                            float zm = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) zm = fmaxf(zm, __shfl_xor_sync(FULL, zm, o));
+                            float xm = 0.f, ym = 0.f;
+                            const float p0 = exp2f(z[e] - zm), p1 = exp2f(z[2 + e] - zm);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                xm = fmaxf(xm, fmaxf(p0 * P.s[0][g], p1 * P.s[1][g]));
+                                ym = fmaxf(ym, fmaxf(p0 * fabsf(P.o[0][g]), p1 * fabsf(P.o[1][g])));
+                            }
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) {
+                                xm = fmaxf(xm, __shfl_xor_sync(FULL, xm, o));
+                                ym = fmaxf(ym, __shfl_xor_sync(FULL, ym, o));
+                            }
+                            // below 2^(exponent + 1)
+                            const int x_up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);
+                            const int y_up = AT_TOP_Y - ((int)(__float_as_uint(ym) >> 23) - 126);
+                            const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), 100)));
+                            corr[e] = exp2f(ref[e] - nr);
+                            ref[e] = nr;
+                            l[e] *= corr[e];
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) off[g][e] *= corr[e];
+                        }
+                        if (NE == 1) corr[1] = corr[0];
+#pragma unroll
+                        for (int k = 0; k < MT; ++k)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                acc[k][v] *= corr[v & 1];
+                                tot[k][v] *= corr[v & 1];
+                            }
+                        weights(Yes{});
+                    }
 #pragma unroll
                     for (int e = 0; e < NE; ++e) {
-                        p[e] = ex2(z[e] - ref[e]);
-                        p[2 + e] = ex2(z[2 + e] - ref[e]);
+                        l[e] += p[e] + p[2 + e];
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            x[g][e] = p[e] * P.s[0][g];
-                            x[g][2 + e] = p[2 + e] * P.s[1][g];
-                            y[g][e] = fmaf(p[e], P.o[0][g], p[2 + e] * P.o[1][g]);
-                            // pages that the head did not select may hold anything
-                            if (masked.value && !keeps<G>(mask, 2 * c + e)) x[g][e] = x[g][2 + e] = y[g][e] = 0.f;
-                            sum = fmaf(fabsf(y[g][e]), AT_MAX_X / AT_MAX_Y, sum + (x[g][e] + x[g][2 + e]));
+                        for (int g = 0; g < NG; ++g) off[g][e] += y[g][e];
+                    }
+                    unsigned w0[WPL], w1[WPL];
+                    const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
+                    load_words<WPL>(vt + c * D + piece, w0);
+                    load_words<WPL>(vt + (c + 4) * D + piece, w1);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        // token by column, to column by token
+                        unsigned bf[NB][2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float x0 = x[g][2 * u], x1 = x[g][2 * u + NE - 1];
+                            const unsigned hi = pack_f16(x0, x1);
+                            const unsigned lo = rest_f16(x0, x1, hi);
+                            if constexpr (G == 8) {
+                                bf[0][u] = transpose8(hi);
+                                bf[1][u] = transpose8(lo);
+                            } else if constexpr (G == 1) {
+                                bf[0][u] = transpose8(__byte_perm(hi, lo, 0x5410));
+                            } else {
+                                bf[0][u] = transpose8(rest ? lo : hi);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 2 * g; k < 2 * g + 2; ++k) {
+                            const unsigned a0 = code_f16<0>(w0[k], one), a1 = code_f16<1>(w0[k], one),
+                                           a2 = code_f16<0>(w1[k], one), a3 = code_f16<1>(w1[k], one);
+#pragma unroll
+                            for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[q][0], bf[q][1]);
+                            const unsigned d0 = code_f16<2>(w0[k], one), d1 = code_f16<3>(w0[k], one),
+                                           d2 = code_f16<2>(w1[k], one), d3 = code_f16<3>(w1[k], one);
+#pragma unroll
+                            for (int q = 0; q < NB; ++q)
+                                mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[q][0], bf[q][1]);
                         }
                     }
-                    return sum;
-                };
-                float sum;
-                const bool all = whole<G>(mask, n);
-                if (all) {
-                    sum = weights(No{});
-                } else {
-                    mask_scores<G>(mask, n, z);
-                    // so may rows behind the sequence
+                    if (--until == 0) {
+                        until = FLUSH;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if (r + 8 * u >= n)
+                        for (int k = 0; k < MT; ++k)
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) P.s[u][g] = P.o[u][g] = 0.f;
-                    sum = weights(Yes{});
-                }
-                if (__any_sync(FULL, !(sum <= AT_MAX_X))) {
-                    // the reference follows the largest p s
-                    float corr[2] = {1.f, 1.f};
-#pragma unroll
-                    for (int e = 0; e < NE; ++e) {
-                        float zm = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) zm = fmaxf(zm, __shfl_xor_sync(FULL, zm, o));
-                        float xm = 0.f, ym = 0.f;
-                        const float p0 = exp2f(z[e] - zm), p1 = exp2f(z[2 + e] - zm);
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            xm = fmaxf(xm, fmaxf(p0 * P.s[0][g], p1 * P.s[1][g]));
-                            ym = fmaxf(ym, fmaxf(p0 * fabsf(P.o[0][g]), p1 * fabsf(P.o[1][g])));
-                        }
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            xm = fmaxf(xm, __shfl_xor_sync(FULL, xm, o));
-                            ym = fmaxf(ym, __shfl_xor_sync(FULL, ym, o));
-                        }
-                        // below 2^(exponent + 1)
-                        const int x_up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);
-                        const int y_up = AT_TOP_Y - ((int)(__float_as_uint(ym) >> 23) - 126);
-                        const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), 100)));
-                        corr[e] = exp2f(ref[e] - nr);
-                        ref[e] = nr;
-                        l[e] *= corr[e];
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) off[g][e] *= corr[e];
+                            for (int v = 0; v < 4; ++v) {
+                                tot[k][v] += acc[k][v];
+                                acc[k][v] = 0.f;
+                            }
                     }
-                    if (NE == 1) corr[1] = corr[0];
-#pragma unroll
-                    for (int k = 0; k < MT; ++k)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            acc[k][v] *= corr[v & 1];
-                            tot[k][v] *= corr[v & 1];
-                        }
-                    weights(Yes{});
-                }
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    l[e] += p[e] + p[2 + e];
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) off[g][e] += y[g][e];
-                }
-                unsigned w0[WPL], w1[WPL];
-                const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
-                load_words<WPL>(vt + c * D + piece, w0);
-                load_words<WPL>(vt + (c + 4) * D + piece, w1);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    // token by column, to column by token
-                    unsigned bf[NB][2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float x0 = x[g][2 * u], x1 = x[g][2 * u + NE - 1];
-                        const unsigned hi = pack_f16(x0, x1);
-                        const unsigned lo = rest_f16(x0, x1, hi);
-                        if constexpr (G == 8) {
-                            bf[0][u] = transpose8(hi);
-                            bf[1][u] = transpose8(lo);
-                        } else if constexpr (G == 1) {
-                            bf[0][u] = transpose8(__byte_perm(hi, lo, 0x5410));
-                        } else {
-                            bf[0][u] = transpose8(rest ? lo : hi);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 2 * g; k < 2 * g + 2; ++k) {
-                        const unsigned a0 = code_f16<0>(w0[k], one), a1 = code_f16<1>(w0[k], one), a2 = code_f16<0>(w1[k], one),
-                                       a3 = code_f16<1>(w1[k], one);
-#pragma unroll
-                        for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[q][0], bf[q][1]);
-                        const unsigned d0 = code_f16<2>(w0[k], one), d1 = code_f16<3>(w0[k], one), d2 = code_f16<2>(w1[k], one),
-                                       d3 = code_f16<3>(w1[k], one);
-#pragma unroll
-                        for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[q][0], bf[q][1]);
-                    }
-                }
-                if (--until == 0) {
-                    until = FLUSH;
-#pragma unroll
-                    for (int k = 0; k < MT; ++k)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            tot[k][v] += acc[k][v];
-                            acc[k][v] = 0.f;
-                        }
                 }
             }
             __syncwarp();
-            if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
+            if (i + RING_STAGES < stages) ring.issue(a, sh, i + RING_STAGES);
         }
         // the share's partial: sums over the lanes of a column and over the
         // columns of a head, through the ring's memory (no copy is in flight)
@@ -861,17 +881,18 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     constexpr int NE = Queries<D, G>::NE;
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
-    __shared__ int2 infos[AT_WARPS][RING_STAGES];
+    __shared__ int2 infos[AT_WARPS][RING_STAGES][4];
     constexpr int EARLY = G == 8 ? 4 : 8;  // tiles a share begins with
     __shared__ float early[AT_WARPS][EARLY * 16 * G];
     __shared__ unsigned early_row[AT_WARPS][EARLY];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * AT_WARPS + warp;
     Ring ring;
-    ring.init(rings + warp * Ring::BYTES, bars[warp], infos[warp]);
+    ring.init(a, rings + warp * Ring::BYTES, bars[warp], infos[warp]);
     const unsigned column = 0x11111111u << c, below = (1u << lane) - 1u;  // lanes of the same columns
     const size_t row_len = (size_t)a.max_pages * a.P;
     Walk walk(a, w);
+    const int page_bytes = (a.ct << a.lc) * Kv4<D>::TILE;
     bool alive = true;  // no wait ran out so far
     while (walk.more(a)) {
         const Share sh = walk.next(a);
@@ -879,7 +900,8 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
         Queries<D, G> Q;
         Q.fetch(a.q + (size_t)h0 * D);
         ring.start();
-        for (int i = 0; i < RING_STAGES && sh.first + i < sh.last && alive; ++i) ring.issue(a, sh, sh.first + i);
+        const int stages = alive ? ring.stages(a, sh) : 0;
+        for (int i = 0; i < RING_STAGES && i < stages; ++i) ring.issue(a, sh, i);
         Q.finish((a.alpha - 1.f) * rsqrtf((float)D));
         const size_t list = (size_t)(h0 + 2 * c) * row_len + (size_t)sh.first * (16 * a.ct);
 
@@ -953,15 +975,15 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
             }
             held = -1;
         };
-        for (int i = sh.first; i < sh.last && alive; ++i) {
-            int2 what;
-            unsigned char *stage;
-            if (!ring.take(a, what, stage)) {
+        for (int i = 0; i < stages; ++i) {
+            const int2 *whats;
+            const unsigned char *stage;
+            if (!ring.take(a, whats, stage)) {
                 ring.drain(a);
                 alive = false;  // the shares end empty, so that what reads them finds them whole
                 break;
             }
-            if (a.zmax && (i & 3) == 3) {  // used four chunks on: nothing waits for the load
+            if (a.zmax && (i & 1)) {  // used two stages on: nothing waits for the load
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     known[e] = fmaxf(known[e], ord2f(next[e]));
@@ -969,29 +991,33 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                     next[e] = __ldcg(a.zmax + h0 + (2 * c + e) % G);
                 }
             }
-            const int mask = what.y >> 8;
-            int left = what.y & 0xff;
-            unsigned row = (unsigned)what.x + r;
 #pragma unroll 1
-            for (const unsigned char *tile = stage; left > 0; left -= 16, tile += Kv4<D>::TILE, row += 16) {
-                float z[4];
-                tile_scores<D, G>(tile, Q, a.one, z);
-                if (!whole<G>(mask, left)) mask_scores<G>(mask, left, z);
-                if (held < 0) {
-                    test(z, row);
-                    continue;
+            for (int page = 0; page < a.npg; ++page, stage += page_bytes) {
+                const int2 what = whats[page];
+                const int mask = what.y >> 8;
+                int left = what.y & 0xff;
+                unsigned row = (unsigned)what.x + r;
+#pragma unroll 1
+                for (const unsigned char *tile = stage; left > 0; left -= 16, tile += Kv4<D>::TILE, row += 16) {
+                    float z[4];
+                    tile_scores<D, G>(tile, Q, a.one, z);
+                    if (!whole<G>(mask, left)) mask_scores<G>(mask, left, z);
+                    if (held < 0) {
+                        test(z, row);
+                        continue;
+                    }
+                    float *to = early[warp] + held * 16 * G;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if ((v & 1) < NE && 2 * c + (v & 1) < G) to[(r + 8 * (v >> 1)) * G + 2 * c + (v & 1)] = z[v];
+                    if (r == 0) early_row[warp][held] = row;
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) m[e] = fmaxf(m[e], fmaxf(z[e], z[2 + e]));
+                    if (++held == EARLY) settle();
                 }
-                float *to = early[warp] + held * 16 * G;
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if ((v & 1) < NE && 2 * c + (v & 1) < G) to[(r + 8 * (v >> 1)) * G + 2 * c + (v & 1)] = z[v];
-                if (r == 0) early_row[warp][held] = row;
-#pragma unroll
-                for (int e = 0; e < NE; ++e) m[e] = fmaxf(m[e], fmaxf(z[e], z[2 + e]));
-                if (++held == EARLY) settle();
             }
             __syncwarp();
-            if (i + RING_STAGES < sh.last) ring.issue(a, sh, i + RING_STAGES);
+            if (i + RING_STAGES < stages) ring.issue(a, sh, i + RING_STAGES);
         }
         if (held >= 0) settle();
         const size_t slot = a.kv0 * slots_per_head(a.B) + sh.slot;
@@ -1002,7 +1028,8 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
             for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
             // a NaN stays a candidate: its share may not be passed over for a low max
             if (__ballot_sync(FULL, bad[e]) & column) m[e] = __int_as_float(0x7fc00000);
-            if (r == 0 && 2 * c + e < G) a.seg[slot * G + 2 * c + e] = make_int4(n[e], __float_as_int(m[e]), sh.first * (16 * a.ct), 0);
+            if (r == 0 && 2 * c + e < G)
+                a.seg[slot * G + 2 * c + e] = make_int4(n[e], __float_as_int(m[e]), sh.first * (16 * a.ct), 0);
         }
     }
 }
@@ -1039,8 +1066,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const GroupShares gs = group_shares(a, b, kvh);
     const int W = gs.n;
     const int4 *seg = a.seg + gs.slot * G + h % G;
-    int *seg_at = dyn + 2 * TK_CAP, *seg_base = seg_at + W + 1;  // place of each share's candidates among the head's, and
-                                                                 // in the head's list
+    // place of each share's candidates among the head's, and in the head's list
+    int *seg_at = dyn + 2 * TK_CAP, *seg_base = seg_at + W + 1;
     const bool fine = __syncthreads_and((qb & 0x7f80u) != 0x7f80u);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
 
@@ -1467,6 +1494,7 @@ int entmaxkv_kv4_decode(const entmaxkv_shape *s, const void *q, const void *k4, 
     kv_range(s, &a.kv0, &a.nk);
     a.ct = s->page_size == 16 ? 1 : 2;
     a.lc = s->page_size == 64 ? 1 : 0;
+    a.npg = 64 / s->page_size;
     a.alpha = alpha;
     a.r_int = alpha > 1.f ? integer_r(alpha) : 0;
     a.one = 0x64006400u;

@@ -231,8 +231,8 @@ struct Stats {
     float mn[PARTS][D], mx[PARTS][D];
 };
 template <int D>
-__device__ __forceinline__ void build_record(const MetaArgs &m, const unsigned char *image, Stats<D> &sh, int b, int kvh,
-                                             int page, int n, unsigned big) {
+__device__ __forceinline__ void build_record(const MetaArgs &m, const unsigned char *image, Stats<D> &sh, int b,
+                                             int kvh, int page, int n, unsigned big) {
     constexpr int PARTS = Stats<D>::PARTS;
     {
         const int q = threadIdx.x % (D / 4), part = threadIdx.x / (D / 4);
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(RW_THREADS) kv4_write_kernel(const __grid_cons
     const int first = j.t0 / RPW<D> + warp;
     fetch(first * RPW<D> + lane / LPR<D>);
     if (meta && j.t0 > 0) {  // the page's old tokens
-        for (int i = threadIdx.x; i < (j.t0 + 15) / 16 * TILE / 16; i += RW_THREADS) cp_async16(image + 16 * i, kt + 16 * i);
+        for (int i = threadIdx.x; i < (j.t0 + 15) / 16 * TILE / 16; i += RW_THREADS)
+            cp_async16(image + 16 * i, kt + 16 * i);
         cp_async_commit();
         cp_async_wait<0>();
         __syncthreads();

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__
     pdl_wait();
     const PageArgs &p = a.p;
     const long long per = (a.bytes + MV_CHUNK - 1) / MV_CHUNK;  // chunks of a block
-    const long long meta0 = p.B, n_meta = FORK ? (long long)a.metas * p.B * a.Hkv * a.n_tiles : 0, move0 = meta0 + n_meta;
+    const long long meta0 = p.B, n_meta = FORK ? (long long)a.metas * p.B * a.Hkv * a.n_tiles : 0;
+    const long long move0 = meta0 + n_meta;
     const long long total = move0 + per * a.bufs * (a.bufs ? *p.n_pairs : 0);
     for (long long k = blockIdx.x; k < total; k += gridDim.x) {
         if (k >= move0) {
@@ -384,7 +385,8 @@ __global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__
             const int b = (int)(i % p.B), m = (int)(i / p.B), from = p.act[b];
             if (from < 0 || (p.in_place && from == b)) continue;
             if ((long long)t * META_TILE * p.P >= seq_len_of(p.lens_in, from, p.P, p.max_pages, nullptr)) continue;
-            const long long s = ((long long)from * a.Hkv + h) * a.n_tiles + t, d = ((long long)b * a.Hkv + h) * a.n_tiles + t;
+            const long long s = ((long long)from * a.Hkv + h) * a.n_tiles + t;
+            const long long d = ((long long)b * a.Hkv + h) * a.n_tiles + t;
 #pragma unroll 1
             for (int r = 0; r < 2; ++r) {
                 const long long base = r ? a.region : 0;
