@@ -266,13 +266,18 @@ __global__ void __launch_bounds__(PL_NT) plan_grow_kernel(const __grid_constant_
             end = used + scan64(max(0, k), tot);
             used += tot;
         }
-        if (k < 0) continue;
         if (end > have && k > 0) {
             atomicOr(a.status, ENTMAXKV_STATUS_NO_BLOCK);
-            continue;
+            k = -1;
         }
-        for (int i = 0; i < k; ++i) a.table_out[(size_t)b * a.max_pages + n0 + i] = list[end - k + i];
-        a.lens_out[b] = (int)L;
+        // the warp's rows one after another, a lane a page
+        for (unsigned some = __ballot_sync(FULL, k > 0); some; some &= some - 1u) {
+            const int l = __ffs(some) - 1, kk = __shfl_sync(FULL, k, l);
+            const long long from = __shfl_sync(FULL, end, l) - kk;
+            int *row = a.table_out + (size_t)__shfl_sync(FULL, b, l) * a.max_pages + __shfl_sync(FULL, n0, l);
+            for (int i = threadIdx.x & 31; i < kk; i += 32) row[i] = list[from + i];
+        }
+        if (k >= 0) a.lens_out[b] = (int)L;
     }
 }
 

@@ -328,6 +328,24 @@ def test_where_the_plan_moves_off_the_chip(B, mp, nb):
 
 
 @gpu
+def test_grow_by_prompts():
+    """Thousands of pages for one row beside rows that need one or none."""
+    B, mp, P, nb = 40, 9000, 16, 30000
+    lens = np.zeros(B, np.int64)
+    lens[5], lens[6] = 31, 32
+    add = np.ones(B, np.int64)
+    add[3], add[7], add[11] = 8999 * 16 + 3, 700 * 16, 0
+    p = Pool(B, P, mp, nb, lens, seed=2, share=False, words=4, bufs=1)
+    want_t, want_l, short = ref.grow(add, p.table, p.lens, P, nb)
+    assert not short
+    table, lens_d = i32(p.table), i32(p.lens)
+    pages.entmaxkv_pages_grow(p.shape, i32(add), table, lens_d, workspace=p.ws)
+    assert nv.get_status() == 0
+    np.testing.assert_array_equal(table.cpu().numpy(), want_t)
+    np.testing.assert_array_equal(lens_d.cpu().numpy(), want_l)
+
+
+@gpu
 def test_grow_without_enough_blocks():
     """Needs are counted in order, those that fail too; a row that needs no block grows all the same."""
     p = Pool(5, 16, 6, 10, [16, 16, 10, 0, 16], share=False)
