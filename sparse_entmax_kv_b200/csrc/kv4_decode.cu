@@ -65,6 +65,9 @@ namespace {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_MAX_WARPS = 148 * 5 * AT_WARPS;
+constexpr int WHOLE_WARPS = 12;         // warps of a CTA that has a group to itself ...
+constexpr int WHOLE_TILES = 16;         // ... and tiles for each of them at most, with many groups
+constexpr int WHOLE_FEW = 5;            // and with few
 constexpr int AT_MIN_CHUNKS = 2;        // chunks a warp gets at least ...
 constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
 constexpr float AT_MAX_X = 32768.f;     // p s stays below this (fp16 ends at 65504) ...
@@ -92,7 +95,7 @@ struct Kv4DecodeArgs {
     int2 *slots;          // [B Hkv] first and last slot of the group's shares
     int *zmax;            // [B Hq] running max of a head's z (order-mapped), null: none kept
     int W;                // warps that share the chunks at most
-    int S;                // with selections: shares of a group
+    int S;                // shares of a group, where every group's list is cut alike (else 0)
     int ct, lc;           // tiles of a chunk (1 or 2), log2 of the chunks of a page
     int npg;              // pages of a ring stage
     int B, Hq, Hkv, P, max_pages, num_blocks;
@@ -184,7 +187,7 @@ struct Walk {
             const int k = w - s.g * a.S;
             group_of(s.g, a.kv0, a.nk, s.b, s.kvh);
             s.bk = s.b * a.Hkv + s.kvh;
-            s.T = entry_chunks(a, s.g);
+            s.T = entry_chunks(a, chosen(a) ? s.g : s.b);
             s.U = s.T >> a.lc;
             s.seq = tokens_of(a, s.b);
             s.first = (int)((long long)s.T * k / a.S);
@@ -233,16 +236,17 @@ struct GroupShares {
 // call on it alone may use, so calls on disjoint ranges share a workspace.
 __host__ __device__ inline size_t slots_per_head(int B) { return (size_t)AT_MAX_WARPS + B; }
 
-// Called by every thread of a head's CTA; also reports what the host cannot see.
+// What the host cannot see: a length or a count beyond the table.
+__device__ __forceinline__ void report_limits(const Kv4DecodeArgs &a, int b, int kvh) {
+    if (__ldg(a.seq_lens + b) > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
+    if (a.sel && (unsigned)__ldg(a.cnt + b * a.Hq + kvh) > (unsigned)n_pages_of(tokens_of(a, b), a.P))
+        atomicOr(a.status, ENTMAXKV_STATUS_BAD_SELECTION);
+}
+// Called by every thread of a head's CTA.
 __device__ __forceinline__ GroupShares group_shares(const Kv4DecodeArgs &a, int b, int kvh) {
     const int2 s = __ldcg(a.slots + b * a.Hkv + kvh);
     const int T = entry_chunks(a, chosen(a) ? b * a.nk + kvh - a.kv0 : b);
-    if (threadIdx.x == 0) {
-        const int len = __ldg(a.seq_lens + b);
-        if (len > a.max_pages * a.P) atomicOr(a.status, ENTMAXKV_STATUS_BAD_LENGTH);
-        if (a.sel && (unsigned)__ldg(a.cnt + b * a.Hq + kvh) > (unsigned)n_pages_of(tokens_of(a, b), a.P))
-            atomicOr(a.status, ENTMAXKV_STATUS_BAD_SELECTION);
-    }
+    if (threadIdx.x == 0) report_limits(a, b, kvh);
     GroupShares r;
     r.n = T > 0 ? s.y - s.x + 1 : 0;
     r.slot = a.kv0 * slots_per_head(a.B) + (T > 0 ? s.x : 0);
@@ -573,8 +577,10 @@ struct No {
 
 // -------------------------------------------------------------- softmax
 
-template <int D, int G>
-__global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>()))
+// WHOLE: the CTA's warps share one group's list, and the CTA writes the result
+// itself; else shares leave partials for combine_kernel.
+template <int D, int G, int WARPS, bool WHOLE>
+__global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>()))
     kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, G>::NE;
@@ -582,10 +588,11 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>()))
     constexpr int FLUSH = 8 / NB;       // tiles between flushes of the output sums
     using Ring = TileRing<D, true>;
     extern __shared__ __align__(128) unsigned char rings[];
-    __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
-    __shared__ int2 infos[AT_WARPS][RING_STAGES][4];
+    __shared__ uint64_t bars[WARPS][RING_STAGES];
+    __shared__ int2 infos[WARPS][RING_STAGES][4];
+    __shared__ float2 parts[WHOLE ? WARPS : 1][G];  // reference and sum of the warps' shares
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    const int w = blockIdx.x * AT_WARPS + warp;
+    const int w = blockIdx.x * WARPS + warp;
     const unsigned one = a.one;
     const bool rest = G == 4 ? c >= 2 : G == 2 ? c & 1 : false;  // the lane's columns carry the lower parts
     Ring ring;
@@ -770,11 +777,12 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>()))
                 for (int g = 0; g < NG; ++g) off[g][e] += __shfl_xor_sync(FULL, off[g][e], o);
             }
         const size_t slot = a.kv0 * slots_per_head(a.B) + sh.slot;
-        if (lane == 0) report_slot(a, sh);
+        if (!WHOLE && lane == 0) report_slot(a, sh);
         if (r == 0)
 #pragma unroll
             for (int e = 0; e < NE; ++e)
-                if (2 * c + e < G) a.part_ml[slot * G + 2 * c + e] = make_float2(ref[e], l[e]);
+                if (2 * c + e < G)
+                    (WHOLE ? parts[warp][2 * c + e] : a.part_ml[slot * G + 2 * c + e]) = make_float2(ref[e], l[e]);
         float *merge = reinterpret_cast<float *>(ring.base);
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
@@ -792,12 +800,46 @@ __global__ void __launch_bounds__(AT_THREADS, (softmax_ctas<D, G>()))
                 if (n < G) merge[n * D + j + (v >> 1)] = o + off[k >> 2][v & 1];
             }
         }
+        if (WHOLE) break;  // the one share
         __syncwarp();
         for (int i = lane; i < G * D / 4; i += 32)
             reinterpret_cast<float4 *>(a.part_o + slot * G * D)[i] = reinterpret_cast<const float4 *>(merge)[i];
         // the next share's copies write over it
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+    }
+    if constexpr (WHOLE) {
+        __shared__ int strange[G];  // heads whose query is not finite
+        int b, kvh;
+        group_of(blockIdx.x, a.kv0, a.nk, b, kvh);
+        const int h0 = b * a.Hq + kvh * G;
+        if (threadIdx.x < G) strange[threadIdx.x] = 0;
+        if (threadIdx.x == 0) report_limits(a, b, kvh);
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * D; i += 32 * WARPS)
+            if ((__ldg(a.q + (size_t)h0 * D + i) & 0x7f80u) == 0x7f80u) strange[i / D] = 1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * D; i += 32 * WARPS) {
+            const int h = i / D;
+            float M = -INFINITY, den = 0.f, num = 0.f;
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) M = fmaxf(M, parts[k][h].x);
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) {
+                const float2 ml = parts[k][h];
+                if (ml.y == 0.f) continue;  // no token of the head (NaN scores make it NaN)
+                const float f = exp2f(ml.x - M);
+                den = fmaf(f, ml.y, den);
+                if (f != 0.f) num = fmaf(f, reinterpret_cast<const float *>(rings + k * Ring::BYTES)[i], num);
+            }
+            const float nan = __int_as_float(0x7fc00000);
+            const bool fine = !strange[h], none = den == 0.f;
+            a.out[(size_t)h0 * D + i] = !fine ? nan : none ? 0.f : num / den;
+            if (i % D == 0) {
+                if (!fine) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
+                if (a.tau_out) a.tau_out[h0 + h] = !fine || none ? nan : 0.6931471805599453f * (M + log2f(den));
+            }
+        }
     }
 }
 
@@ -1393,18 +1435,30 @@ Carve carve(const entmaxkv_shape *s) {
 }
 
 template <class K>
-cudaError_t run_shares(K k, const Kv4DecodeArgs &a, size_t smem, cudaStream_t st) {
-    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k), smem);
-    return e != cudaSuccess ? e : launch_pdl(k, dim3(ceil_div(a.W, AT_WARPS)), dim3(AT_THREADS), smem, st, a);
+cudaError_t run_shares(K k, const Kv4DecodeArgs &a, int warps, size_t ring, cudaStream_t st) {
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k), warps * ring);
+    return e != cudaSuccess ? e : launch_pdl(k, dim3(ceil_div(a.W, warps)), dim3(32 * warps), warps * ring, st, a);
 }
 
 template <int D, int G>
 cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
-    const int heads = a.B * a.nk * G;
+    const int groups = a.B * a.nk, heads = groups * G;
     cudaError_t e;
     if (a.alpha == 1.f) {
+        constexpr size_t ring = TileRing<D, true>::BYTES;
+        // Short lists, or enough groups that a CTA for each fills the GPU: one
+        // launch, each CTA a group.  us, so and cut over the GPU: 2 groups of
+        // 701 tokens 11.3 and 15.6 (one call after another, the host's time
+        // counts), 64 of 1500 16.5 and 20.6, 128 of 3000 23.2 and 27.3; but 16
+        // of 1500 18.5 and 16.6, 8 of 3000 20.6 and 14.4
+        const int tiles = a.max_pages * (a.ct << a.lc);
+        if (groups <= sms && tiles <= WHOLE_WARPS * (3 * groups >= sms ? WHOLE_TILES : WHOLE_FEW)) {
+            a.S = WHOLE_WARPS;
+            a.W = groups * WHOLE_WARPS;
+            return run_shares(kv4_softmax_kernel<D, G, WHOLE_WARPS, true>, a, WHOLE_WARPS, ring, st);
+        }
         share_out(a, sms, softmax_ctas<D, G>());
-        e = run_shares(kv4_softmax_kernel<D, G>, a, AT_WARPS * TileRing<D, true>::BYTES, st);
+        e = run_shares(kv4_softmax_kernel<D, G, AT_WARPS, false>, a, AT_WARPS, ring, st);
         if (e != cudaSuccess) return e;
         // heads of many shares get more threads while every SM has a place for
         // one (24 heads of 512 shares: 31 us in all with 1024 threads, 49 with
@@ -1421,7 +1475,7 @@ cudaError_t decode_t(Kv4DecodeArgs a, int sms, cudaStream_t st) {
         e = launch_pdl(kv4_reset_kernel, dim3(ceil_div(heads, 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
-    if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS * TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
+    if ((e = run_shares(kv4_scan_kernel<D, G>, a, AT_WARPS, TileRing<D, false>::BYTES, st)) != cudaSuccess) return e;
     const size_t smem = (size_t)(2 * TK_CAP + 2 * a.W + 1) * 4;
     // More threads a head while every head's CTA finds a place at once (128
     // heads: 22 us with 512 threads, 25 with 256; 512 heads: 19 and 11)

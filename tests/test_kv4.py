@@ -317,6 +317,29 @@ def test_decode_every_page(alpha, G, Hkv, d, P):
 
 
 @gpu
+@pytest.mark.parametrize("B", [1, 5, 30, 80])
+@pytest.mark.parametrize("G,Hkv,d,P", [(1, 2, 64, 16), (2, 2, 128, 32), (4, 2, 64, 64), (8, 2, 128, 16)])
+def test_short_sequences(B, G, Hkv, d, P):
+    """Softmax of sequences that one CTA takes whole, up to the lengths and numbers of groups where it stops."""
+    rng = np.random.RandomState(B)
+    lens = rng.randint(0, 400, B)
+    lens[0] = 930 if B == 1 else 0
+    lens[-1] = 1  # the table: 58 pages of 16 and one more
+    if B == 80:
+        lens[5] = 2900
+    c = Case(B, G * Hkv, Hkv, d, P, [int(x) for x in lens] if B > 1 else [930], seed=B)
+    c.q[-1, 0, 3] = float("inf")
+    c.write(meta=False)
+    nv.get_status(clear=True)
+    out, tau = c.decode(1.0)
+    assert nv.get_status(clear=True) == nv.STATUS_NONFINITE
+    assert out[-1, 0].isnan().all() and bool(tau[-1, 0].isnan())
+    c.q[-1, 0, 3] = 0.0
+    out, tau = c.decode(1.0)
+    c.check_decode(1.0, out, tau)
+
+
+@gpu
 @pytest.mark.parametrize("alpha", [1.0, 1.5, 2.0])
 @pytest.mark.parametrize("G,Hkv,d,P", [(1, 2, 64, 16), (4, 2, 128, 32), (8, 1, 128, 64)])
 def test_decode_kept_pages(alpha, G, Hkv, d, P):
