@@ -44,8 +44,8 @@
 // with its values and 260 without, most of them to make operands of codes; the
 // integer pipe is 50 to 55 % busy, the issue slots 60 to 65 %, the tensor
 // pipe 15 %.  Softmax over 8 sequences of 16k to 32k tokens, 8 kv heads of 4,
-// d = 128: 71 us, 236 MB at 3.3 TB/s (50 % of a copy's rate); entmax over 4
-// of 64k to 128k: 122 us, of which the scan is 105 (271 MB at 2.6 TB/s).
+// d = 128: 72 us, 236 MB at 3.3 TB/s (50 % of a copy's rate); entmax over 4
+// of 64k to 128k: 119 us, of which the scan is 100 (271 MB at 2.7 TB/s).
 // Tried and dropped: units of a quarter of a warp's share, taken from a queue
 // in one CTA an SM (71 -> 84 us, 126 -> 145: each pays for its queries and its
 // first copies again); key codes uncentred, straight from the mask (4 to 6 %

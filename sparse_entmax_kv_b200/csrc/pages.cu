@@ -354,21 +354,26 @@ __device__ __forceinline__ void move_chunk(const char *from, char *to, long long
         if (u * MV_NT + threadIdx.x < m) dst[u * MV_NT + threadIdx.x] = v[u];
 }
 
+// Buffers that a launch has room for: its arguments are copied with it, and
+// few buffers are the common case.
+constexpr int FEW = 16;
+
+template <int N>
 struct ApplyArgs {
     PageArgs p;
     int bufs, metas;
     long long bytes;  // of a block
     int Hkv, n_tiles;
     long long region, tile[2];  // bytes of the bound region, and of a tile in it and in the other
-    char *buf[ENTMAXKV_MAX_BUFFERS];
-    const char *meta_in[ENTMAXKV_MAX_BUFFERS];
-    char *meta_out[ENTMAXKV_MAX_BUFFERS];
+    char *buf[N];
+    const char *meta_in[N];
+    char *meta_out[N];
 };
 
 // Rows, then metadata tiles (of both regions; they follow their rows), then
 // chunks of the block pairs, item after item.
-template <bool FORK>
-__global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__ ApplyArgs a) {
+template <bool FORK, int N>
+__global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__ ApplyArgs<N> a) {
     pdl_wait();
     const PageArgs &p = a.p;
     const long long per = (a.bytes + MV_CHUNK - 1) / MV_CHUNK;  // chunks of a block
@@ -405,9 +410,10 @@ __global__ void __launch_bounds__(MV_NT, 4) apply_kernel(const __grid_constant__
     }
 }
 
+template <int N>
 struct MoveArgs {
-    const char *src[ENTMAXKV_MAX_BUFFERS];
-    char *dst[ENTMAXKV_MAX_BUFFERS];
+    const char *src[N];
+    char *dst[N];
     const int *src_ids, *dst_ids;
     int n, bufs, src_blocks, dst_blocks;
     long long bytes;   // of a block
@@ -415,7 +421,8 @@ struct MoveArgs {
 };
 
 // Block pairs, every buffer: chunk after chunk of MV_CHUNK bytes.
-__global__ void __launch_bounds__(MV_NT) move_kernel(const __grid_constant__ MoveArgs a) {
+template <int N>
+__global__ void __launch_bounds__(MV_NT) move_kernel(const __grid_constant__ MoveArgs<N> a) {
     pdl_wait();
     const long long per = (a.bytes + MV_CHUNK - 1) / MV_CHUNK;  // chunks of a block
     const long long total = per * a.bufs * a.n;
@@ -534,10 +541,10 @@ cudaError_t plan(K k, PageArgs &a, cudaStream_t st) {
 }
 
 // The second launch; pairs: how many blocks move at most.
-template <bool FORK>
-cudaError_t apply(const PageArgs &p, const entmaxkv_buffers *bufs, const entmaxkv_shape *s, long long pairs,
+template <bool FORK, int N>
+cudaError_t apply_n(const PageArgs &p, const entmaxkv_buffers *bufs, const entmaxkv_shape *s, long long pairs,
                   const entmaxkv_buffers *meta_in, const entmaxkv_buffers *meta_out, cudaStream_t st) {
-    ApplyArgs a;
+    ApplyArgs<N> a;
     a.p = p;
     a.bufs = bufs->count;
     a.bytes = bufs->count ? bufs->block_bytes : 0;
@@ -555,7 +562,34 @@ cudaError_t apply(const PageArgs &p, const entmaxkv_buffers *bufs, const entmaxk
     static_assert(256 * 128 <= MV_CHUNK, "a metadata tile is one chunk");
     const long long items = s->B + (long long)a.metas * s->B * s->Hkv * a.n_tiles +
                             (a.bytes + MV_CHUNK - 1) / MV_CHUNK * a.bufs * pairs;
-    return launch_pdl(apply_kernel<FORK>, dim3((unsigned)(items < GRID ? items : GRID)), dim3(MV_NT), 0, st, a);
+    return launch_pdl(apply_kernel<FORK, N>, dim3((unsigned)(items < GRID ? items : GRID)), dim3(MV_NT), 0, st, a);
+}
+template <bool FORK>
+cudaError_t apply(const PageArgs &p, const entmaxkv_buffers *bufs, const entmaxkv_shape *s, long long pairs,
+                  const entmaxkv_buffers *meta_in, const entmaxkv_buffers *meta_out, cudaStream_t st) {
+    const bool few = bufs->count <= FEW && (!meta_in || meta_in->count <= FEW);
+    return few ? apply_n<FORK, FEW>(p, bufs, s, pairs, meta_in, meta_out, st)
+               : apply_n<FORK, ENTMAXKV_MAX_BUFFERS>(p, bufs, s, pairs, meta_in, meta_out, st);
+}
+
+template <int N>
+cudaError_t move(const entmaxkv_buffers *src, int src_blocks, const entmaxkv_buffers *dst, int dst_blocks,
+                 const int *src_ids, const int *dst_ids, int n, int *status, cudaStream_t st) {
+    MoveArgs<N> m;
+    m.bufs = src->count;
+    m.bytes = src->block_bytes;
+    for (int i = 0; i < src->count; ++i) {
+        m.src[i] = static_cast<const char *>(src->base[i]);
+        m.dst[i] = static_cast<char *>(dst->base[i]);
+    }
+    m.src_ids = src_ids;
+    m.dst_ids = dst_ids;
+    m.n = n;
+    m.src_blocks = src_blocks;
+    m.dst_blocks = dst_blocks;
+    m.status = status;
+    const long long chunks = (m.bytes + MV_CHUNK - 1) / MV_CHUNK * m.bufs * n;
+    return launch_pdl(move_kernel<N>, dim3((unsigned)(chunks < GRID ? chunks : GRID)), dim3(MV_NT), 0, st, m);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
@@ -658,22 +692,8 @@ int entmaxkv_pages_copy(const entmaxkv_buffers *src, int32_t src_blocks, const e
     if (!src_ids || !dst_ids) return ENTMAXKV_ERR_NULL;
     DevInfo di;
     if ((rc = device_info(&di))) return rc;
-    MoveArgs m;
-    m.bufs = src->count;
-    m.bytes = src->block_bytes;
-    for (int i = 0; i < src->count; ++i) {
-        m.src[i] = static_cast<const char *>(src->base[i]);
-        m.dst[i] = static_cast<char *>(dst->base[i]);
-    }
-    m.src_ids = src_ids;
-    m.dst_ids = dst_ids;
-    m.n = n;
-    m.src_blocks = src_blocks;
-    m.dst_blocks = dst_blocks;
-    m.status = di.status;
-    const long long chunks = (m.bytes + MV_CHUNK - 1) / MV_CHUNK * m.bufs * n;
-    return rc_of(launch_pdl(move_kernel, dim3((unsigned)(chunks < GRID ? chunks : GRID)), dim3(MV_NT), 0,
-                            static_cast<cudaStream_t>(stream), m));
+    auto run = src->count <= FEW ? move<FEW> : move<ENTMAXKV_MAX_BUFFERS>;
+    return rc_of(run(src, src_blocks, dst, dst_blocks, src_ids, dst_ids, n, di.status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -184,6 +184,37 @@ def test_fork(B, lens, parent, hold):
 
 
 @gpu
+@pytest.mark.parametrize("bufs,metas", [(17, 1), (2, 17)])
+def test_many_buffers(bufs, metas):
+    """Beyond the numbers of buffers that the small launches have room for: fork, and compaction."""
+    p = Pool(3, 16, 4, 30, [20, 35, 1], seed=3, bufs=bufs)
+    parent = [1, 1, 0]
+    want_t, want_l, pairs, _ = ref.fork(parent, p.table, p.lens, 16, 30)
+    want = p.host_data()
+    for s, d in pairs:
+        want[:, d] = want[:, s]
+    n = nv.meta_bytes(p.shape)
+    a = torch.randint(0, 256, (metas, n), dtype=torch.uint8, device="cuda")
+    o = torch.zeros_like(a)
+    t_out, l_out = i32(np.zeros((3, 4))), i32([0] * 3)
+    pages.entmaxkv_pages_fork(p.shape, i32(parent), i32(p.table), i32(p.lens), t_out, l_out, p.buffers,
+                              pages.Buffers(a.unbind(0)), pages.Buffers(o.unbind(0)), workspace=p.ws)
+    np.testing.assert_array_equal(t_out.cpu().numpy(), want_t)
+    np.testing.assert_array_equal(p.host_data(), want)
+    cut = 3 * 128 * 64
+    for base, size in ((0, 128 * 64), (cut, 256 * 64)):
+        for b, q in enumerate(parent):
+            assert torch.equal(o[:, base + b * size:base + (b + 1) * size], a[:, base + q * size:base + (q + 1) * size])
+    want_t, remap, live, pairs = ref.compact(want_t, want_l, 16, 30)
+    for s, d in pairs:
+        want[:, d] = want[:, s]
+    r_out, n_live = i32([0] * 30), i32([0])
+    pages.entmaxkv_pages_compact(p.shape, t_out, l_out, t_out, p.buffers, r_out, n_live, workspace=p.ws)
+    assert int(n_live) == live and nv.get_status() == 0
+    np.testing.assert_array_equal(p.host_data(), want)
+
+
+@gpu
 def test_fork_without_enough_blocks():
     p = Pool(4, 16, 3, 6, [20, 0, 0, 0], share=False)
     parent = [0, 0, 0, 0]
@@ -385,7 +416,7 @@ def test_compact(B, nb, words, in_place):
 
 
 @gpu
-@pytest.mark.parametrize("nb,words,n,bufs", [(5, 4, 1, 1), (40, 4096 + 4, 17, 3), (9, 33000, 9, 5), (700, 12, 700, 2)])
+@pytest.mark.parametrize("nb,words,n,bufs", [(5, 4, 1, 1), (40, 4096 + 4, 17, 3), (9, 33000, 9, 5), (700, 12, 700, 2), (6, 8, 4, 17)])
 def test_copy(nb, words, n, bufs):
     g = torch.Generator().manual_seed(nb)
     a = torch.randint(-9, 9, (bufs, nb, words), dtype=torch.int32).cuda()
