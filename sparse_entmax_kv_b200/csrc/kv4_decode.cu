@@ -40,12 +40,12 @@
 //            the support
 //
 // What bounds it: instructions, then memory.  A 16-token tile of 128
-// coordinates (2304 bytes with its values) takes about 420 warp instructions
-// with its values and 260 without, most of them to make operands of codes; the
-// integer pipe is 50 to 55 % busy, the issue slots 60 to 65 %, the tensor
-// pipe 15 %.  Softmax over 8 sequences of 16k to 32k tokens, 8 kv heads of 4,
-// d = 128: 72 us, 236 MB at 3.3 TB/s (50 % of a copy's rate); entmax over 4
-// of 64k to 128k: 119 us, of which the scan is 100 (271 MB at 2.7 TB/s).
+// coordinates (2304 bytes with its values) takes about 400 warp instructions
+// with its values and 242 without, most of them to make operands of codes; the
+// integer pipe is 45 to 48 % busy, the issue slots 60 to 65 %, the tensor
+// pipe 16 to 20 %.  Softmax over 8 sequences of 16k to 32k tokens, 8 kv heads of 4,
+// d = 128: 68 us, 236 MB at 3.5 TB/s (53 % of a copy's rate); entmax over 4
+// of 64k to 128k: 117 us, of which the scan is 100 (271 MB at 2.7 TB/s).
 // Tried and dropped: units of a quarter of a warp's share, taken from a queue
 // in one CTA an SM (71 -> 84 us, 126 -> 145: each pays for its queries and its
 // first copies again); key codes uncentred, straight from the mask (4 to 6 %
@@ -147,6 +147,7 @@ struct Walk {
     int i;             // entry of chunk t or before,
     int T;             // the chunks of each of its groups,
     long long start;   // its first chunk
+    Walk() = default;
     __device__ __forceinline__ Walk(const Kv4DecodeArgs &a, int w) {
         this->w = w;
         t = end = 0;
@@ -219,6 +220,22 @@ struct Walk {
         s.opens = s.first == 0;
         s.closes = s.last == T;
         return s;
+    }
+};
+
+// Where a warp is.  It lies in shared memory while the warp reads a share's tiles,
+// whose loop wants the registers: 8 x 32k softmax 75.4 -> 72.2 us, 4 x 128k entmax
+// 124.2 -> 122.1 us.
+struct Place {
+    Walk walk;
+    Share share;
+    __device__ __forceinline__ void put(const Walk &w, const Share &s, int lane) {
+        __syncwarp();
+        if (lane == 0) {
+            walk = w;
+            share = s;
+        }
+        __syncwarp();
     }
 };
 
@@ -590,6 +607,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[WARPS][RING_STAGES];
     __shared__ int2 infos[WARPS][RING_STAGES][4];
+    __shared__ Place places[WHOLE ? 1 : WARPS];
     __shared__ float2 parts[WHOLE ? WARPS : 1][G];  // reference and sum of the warps' shares
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     const int w = blockIdx.x * WARPS + warp;
@@ -601,7 +619,9 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
     const int page_bytes = (a.ct << a.lc) * Kv4<D>::TILE;
     bool alive = true;  // no wait ran out so far
     while (walk.more(a)) {
-        const Share sh = walk.next(a);
+        const Share to_do = walk.next(a);
+        if (!WHOLE) places[warp].put(walk, to_do, lane);
+        const Share &sh = WHOLE ? to_do : places[warp].share;
         Queries<D, G> Q;
         Q.fetch(a.q + ((size_t)sh.b * a.Hq + sh.kvh * G) * D);
         ring.start();
@@ -801,6 +821,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
             }
         }
         if (WHOLE) break;  // the one share
+        walk = places[warp].walk;
         __syncwarp();
         for (int i = lane; i < G * D / 4; i += 32)
             reinterpret_cast<float4 *>(a.part_o + slot * G * D)[i] = reinterpret_cast<const float4 *>(merge)[i];
@@ -924,6 +945,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[AT_WARPS][RING_STAGES];
     __shared__ int2 infos[AT_WARPS][RING_STAGES][4];
+    __shared__ Place places[AT_WARPS];
     constexpr int EARLY = G == 8 ? 8 : 16;  // tiles a share begins with (8: 2 % slower)
     __shared__ float early[AT_WARPS][EARLY * 16 * G];
     __shared__ unsigned early_row[AT_WARPS][EARLY];
@@ -937,7 +959,9 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
     const int page_bytes = (a.ct << a.lc) * Kv4<D>::TILE;
     bool alive = true;  // no wait ran out so far
     while (walk.more(a)) {
-        const Share sh = walk.next(a);
+        const Share to_do = walk.next(a);
+        places[warp].put(walk, to_do, lane);
+        const Share &sh = places[warp].share;
         const int h0 = sh.b * a.Hq + sh.kvh * G;
         Queries<D, G> Q;
         Q.fetch(a.q + (size_t)h0 * D);
@@ -1062,6 +1086,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
             if (i + RING_STAGES < stages) ring.issue(a, sh, i + RING_STAGES);
         }
         if (held >= 0) settle();
+        walk = places[warp].walk;
         const size_t slot = a.kv0 * slots_per_head(a.B) + sh.slot;
         if (lane == 0) report_slot(a, sh);
 #pragma unroll
