@@ -33,7 +33,11 @@ class Buffers:
         self.tensors = tuple(tensors)
         if len(self.tensors) > MAX_BUFFERS:
             raise ValueError(f"at most {MAX_BUFFERS} buffers, got {len(self.tensors)}")
+        if num_blocks is not None and num_blocks < 1:
+            raise ValueError(f"buffers: at least one block, got {num_blocks}")
         for t in self.tensors:
+            if t.numel() == 0 or t.dim() == 0:
+                raise ValueError("buffers: must hold at least one block")
             if t.device.type != "cuda" and not t.is_pinned():
                 raise ValueError("buffers: CUDA or pinned host tensors")
             if not t.is_contiguous():

@@ -387,6 +387,16 @@ def test_unusual_alphas(alpha):
 
 
 @gpu
+@pytest.mark.parametrize("alpha", [1.001, 1.01, 30.0, 1000.0])
+def test_alphas_far_from_the_usual_ones(alpha):
+    c = Case(2, 4, 2, 64, 16, [900, 1], seed=14)
+    c.write(meta=False)
+    out, tau = c.decode(alpha)
+    c.check_decode(alpha, out, tau)
+    assert nv.get_status() == 0
+
+
+@gpu
 def test_values_that_grow_along_the_sequence():
     """The reference of the softmax has to follow p s wherever it rises: steps 2^60 apart, scores 40 apart."""
     def rows(k, v):

@@ -102,6 +102,12 @@ def test_buffers_check_what_they_are_given():
         pages.Buffers([x])
     with pytest.raises(ValueError, match="at most"):
         pages.Buffers([x] * 257)
+    for empty in (torch.zeros(0, 16), torch.zeros(4, 0), torch.tensor(1.0)):
+        with pytest.raises(ValueError, match="at least one block"):
+            pages.Buffers([empty])
+    for n in (0, -4):
+        with pytest.raises(ValueError, match="at least one block"):
+            pages.Buffers([x], num_blocks=n)
     assert pages.Buffers([]).c.count == 0
 
 
