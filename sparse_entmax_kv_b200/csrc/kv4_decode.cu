@@ -19,7 +19,7 @@
 //           and sum_t p_t (lo_tg + 8 s_tg) is added at the end.  The
 //           reference of a head's softmax is placed so that its largest p s
 //           lies between 2^9 and 2^15: what is lost of a weight is below 2^-34
-//           of the largest (values below 2^-90 get less).  Groups of four heads or fewer put the two parts
+//           of the largest (values below 2^-86 get less).  Groups of four heads or fewer put the two parts
 //           in the columns their heads leave free.  The sums move to a second
 //           set of fp32 registers every few tiles, so that few truncations
 //           meet a large sum.
@@ -74,8 +74,10 @@ constexpr int AT_MIN_CHUNKS = 2;        // chunks a warp gets at least ...
 constexpr int AT_GROUP_PARTS = 512;     // ... and warps a group's list is cut among at most, on average
 constexpr float AT_MAX_X = 32768.f;     // p s stays below this (fp16 ends at 65504) ...
 constexpr int AT_TOP_X = 10;            // ... and is brought to 2^10 where a reference is set;
-constexpr float AT_MAX_Y = 0x1p115f;    // so for p |lo + 8 s|, which matters where steps are far below the values
-constexpr int AT_TOP_Y = 100;
+constexpr float AT_MAX_Y = 0x1p103f;    // so for p |lo + 8 s|, which matters where steps are far below the values,
+constexpr int AT_TOP_Y = 96;            // and for p itself, which is all there is where values are zero.
+constexpr int AT_UNIT = 8;              // Sums of the two are kept in units of 2^8: a list has fewer than 2^31 tokens,
+constexpr float AT_PER_UNIT = 1.f / (1 << AT_UNIT);  // so they stay below 2^126
 
 // CTAs an SM holds (registers bound the softmax, shared memory allows five).
 template <int D, int G>
@@ -675,6 +677,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                                 if (masked.value && !keeps<G>(mask, 2 * c + e)) x[g][e] = x[g][2 + e] = y[g][e] = 0.f;
                                 sum = fmaf(fabsf(y[g][e]), AT_MAX_X / AT_MAX_Y, sum + (x[g][e] + x[g][2 + e]));
                             }
+                            sum = fmaf(p[e] + p[2 + e], AT_MAX_X / AT_MAX_Y, sum);
                         }
                         return sum;
                     };
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                         sum = weights(Yes{});
                     }
                     if (__any_sync(FULL, !(sum <= AT_MAX_X))) {
-                        // the reference follows the largest p s
+                        // the reference follows the largest p s, or p, or p |lo + 8 s|
                         float corr[2] = {1.f, 1.f};
 #pragma unroll
                         for (int e = 0; e < NE; ++e) {
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                             // below 2^(exponent + 1)
                             const int x_up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);
                             const int y_up = AT_TOP_Y - ((int)(__float_as_uint(ym) >> 23) - 126);
-                            const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), 100)));
+                            const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), AT_TOP_Y)));
                             corr[e] = exp2f(ref[e] - nr);
                             ref[e] = nr;
                             l[e] *= corr[e];
@@ -734,9 +737,9 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                     }
 #pragma unroll
                     for (int e = 0; e < NE; ++e) {
-                        l[e] += p[e] + p[2 + e];
+                        l[e] = fmaf(p[e] + p[2 + e], AT_PER_UNIT, l[e]);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) off[g][e] += y[g][e];
+                        for (int g = 0; g < NG; ++g) off[g][e] = fmaf(y[g][e], AT_PER_UNIT, off[g][e]);
                     }
                     unsigned w0[WPL], w1[WPL];
                     const int piece = (r ^ kv4_vswz<D>(c)) * (4 * WPL);  // pairs c and c + 4 have the same swizzle
@@ -819,7 +822,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                 if (G == 2) o += __shfl_xor_sync(FULL, o, 1);
                 if (G == 4) o += __shfl_xor_sync(FULL, o, 2);
                 const int n = 2 * c + (v & 1);
-                if (n < G) merge[n * D + j + (v >> 1)] = o + off[k >> 2][v & 1];
+                if (n < G) merge[n * D + j + (v >> 1)] = fmaf(o, AT_PER_UNIT, off[k >> 2][v & 1]);
             }
         }
         if (WHOLE) break;  // the one share
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
             a.out[(size_t)h0 * D + i] = !fine ? nan : none ? 0.f : num / den;
             if (i % D == 0) {
                 if (!fine) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
-                if (a.tau_out) a.tau_out[h0 + h] = !fine || none ? nan : 0.6931471805599453f * (M + log2f(den));
+                if (a.tau_out) a.tau_out[h0 + h] = !fine || none ? nan : 0.6931471805599453f * (M + (AT_UNIT + log2f(den)));
             }
         }
     }
@@ -917,15 +920,16 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     __syncthreads();
     const float nan = __int_as_float(0x7fc00000);
     if (!fine && threadIdx.x == 0) atomicOr(a.status, ENTMAXKV_STATUS_NONFINITE);
-    // den is 0 only without tokens (a share with tokens has a weight of 2^-120
-    // at least); NaN scores make it NaN
+    // den is 0 only without tokens (a share with tokens has a weight of 2^-128
+    // at least, in units of 2^AT_UNIT); NaN scores make it NaN
     const bool none = den == 0.f;
     if (sub == 0) {
 #pragma unroll
         for (int i = 1; i < SUB; ++i) num += o_sh[i][j];
         a.out[(size_t)bh * D + j] = !fine ? nan : none ? 0.f : num / den;
     }
-    if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = !fine || none ? nan : 0.6931471805599453f * (M + log2f(den));
+    if (threadIdx.x == 0 && a.tau_out)
+        a.tau_out[bh] = !fine || none ? nan : 0.6931471805599453f * (M + (AT_UNIT + log2f(den)));
 }
 
 // --------------------------------------------------------------- entmax

@@ -1,0 +1,89 @@
+"""The 4-bit cache where ranges end: values without a step, scores and values of any size, steps on a rounding's
+border, and outputs held to bounds that no wrong output meets."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_bounds as exact
+from sparse_entmax_kv_b200 import kv4, native as nv
+from test_kv4 import Case, f64_of
+
+gpu = pytest.mark.gpu
+
+
+def head_of(c, b, h, alpha, tok=None):
+    """What exact.attention gives for head h of sequence b of a Case."""
+    rows, kvh = c.rows_of(b), h // (c.Hq // c.Hkv)
+    tok = slice(None) if tok is None else tok
+    k, v = (exact.quantise(f64_of(x[rows][:, kvh])[tok]) for x in (c.k, c.v))
+    return exact.attention(f64_of(c.q[b, h]), k, v, alpha)
+
+
+def check(c, alpha, out, tau, sharp=True):
+    """Every head within its bounds; sharp: bounds that an output of zeros, or of another head, does not meet."""
+    out, tau = f64_of(out), f64_of(tau)
+    for b in range(c.B):
+        for h in range(c.Hq):
+            o, t, do, dt = head_of(c, b, h, alpha)
+            assert (np.abs(out[b, h] - o) <= do).all(), (b, h, np.abs(out[b, h] - o).max(), do.max())
+            assert abs(tau[b, h] - t) <= dt, (b, h, tau[b, h], t, dt)
+            if sharp:
+                assert (np.abs(o) > 4 * do).any() and (np.abs(np.roll(o, 1) - o) > 4 * do).any(), (b, h)
+
+
+def prescribe(scores, zero=None, big=None):
+    """rows for Case: key t gives a query of ones the score sqrt(d) scores[t] (constant keys: s = 0, lo the value);
+    values of tokens in `zero` are zero, those of tokens in `big` larger by a factor."""
+    def rows(k, v):
+        k[:] = scores[:, None, None]
+        if zero is not None:
+            v[zero] = 0.0
+        if big is not None:
+            v[big[0]] *= big[1]
+    return rows
+
+
+# ------------------------------------------------------------------ softmax weights of value rows without a step
+
+@gpu
+@pytest.mark.parametrize("G,d,P", [(1, 64, 16), (4, 64, 16), (2, 128, 32), (8, 128, 64)])
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("rise", [15.0, 18.0, 19.0, 24.0, 60.0])
+def test_rising_scores_of_zero_values(G, d, P, long, rise):
+    """Rows of zeros (padding, sinks) carry weight but no p s: their weights have to stay in range by themselves.
+    Tiles of score 0, of `rise` and of rise + 2 (natural units), the first two with values of zero, in every order;
+    the list is one CTA's, or cut over the GPU."""
+    L = 5000 if long else 900
+    at = np.random.RandomState(int(rise) + G).randint(0, 3, -(-L // 16)).repeat(16)[:L]
+    scores = torch.tensor([0.0, rise, rise + 2])[at] / np.sqrt(d)
+    c = Case(1, G, 1, d, P, [L], seed=G, rows=prescribe(scores, zero=torch.from_numpy(at < 2)))
+    c.q[:] = 1.0
+    c.write(meta=False)
+    check(c, 1.0, *c.decode(1.0))
+
+
+@gpu
+@pytest.mark.parametrize("step", [20.0, 27.0])
+def test_runs_of_zero_values(step):
+    """Runs of 64 zero tiles, the scores of each run `step` (powers of two) above the last, then values of their own."""
+    L = 16 * 64 * 6
+    run = np.arange(L) // 1024
+    scores = torch.from_numpy(run * (step * np.log(2) / 8)).float()
+    c = Case(1, 2, 1, 64, 16, [L], rows=prescribe(scores, zero=torch.from_numpy(run < 5)))
+    c.q[:] = 1.0
+    c.write(meta=False)
+    check(c, 1.0, *c.decode(1.0))
+
+
+@gpu
+@pytest.mark.parametrize("value", [0.0, 1.0])
+@pytest.mark.parametrize("L", [900, 40000])
+def test_values_without_a_step(value, L):
+    """All values zero, or all one: the output is that value, and the log-sum-exp is finite and right."""
+    def rows(k, v):
+        v[:] = value
+    c = Case(1, 4, 1, 64, 16, [L], seed=1, rows=rows)
+    c.write(meta=False)
+    out, tau = c.decode(1.0)
+    check(c, 1.0, out, tau, sharp=False)
+    assert (out - value).abs().max() <= 2.0 ** -18
