@@ -598,6 +598,12 @@ struct No {
 
 // -------------------------------------------------------------- softmax
 
+// 2^(x / 2).  References lie 96 above the largest score of their tokens (zero
+// values) to 120 below it (values near 2^128): between two of them a weight's
+// exponent may pass fp32's, though its product with the sum that it brings to
+// the other reference does not.  Sums are therefore multiplied by the root twice.
+__device__ __forceinline__ float half_weight(float x) { return exp2f(0.5f * x); }
+
 // WHOLE: the CTA's warps share one group's list, and the CTA writes the result
 // itself; else shares leave partials for combine_kernel.
 template <int D, int G, int WARPS, bool WHOLE>
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                     }
                     if (__any_sync(FULL, !(sum <= AT_MAX_X))) {
                         // the reference follows the largest p s, or p, or p |lo + 8 s|
-                        float corr[2] = {1.f, 1.f};
+                        float corr[2] = {1.f, 1.f};  // of the sums of p s, which are too small to count where it underflows
 #pragma unroll
                         for (int e = 0; e < NE; ++e) {
                             float zm = fmaxf(z[e], z[2 + e]);
@@ -719,11 +725,12 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                             const int x_up = AT_TOP_X - ((int)(__float_as_uint(xm) >> 23) - 126);
                             const int y_up = AT_TOP_Y - ((int)(__float_as_uint(ym) >> 23) - 126);
                             const float nr = fmaxf(ref[e], zm - (float)max(-120, min(min(x_up, y_up), AT_TOP_Y)));
-                            corr[e] = exp2f(ref[e] - nr);
+                            const float half = half_weight(ref[e] - nr);
+                            corr[e] = half * half;
                             ref[e] = nr;
-                            l[e] *= corr[e];
+                            l[e] = l[e] * half * half;
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) off[g][e] *= corr[e];
+                            for (int g = 0; g < NG; ++g) off[g][e] = off[g][e] * half * half;
                         }
                         if (NE == 1) corr[1] = corr[0];
 #pragma unroll
@@ -854,9 +861,9 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
             for (int k = 0; k < WARPS; ++k) {
                 const float2 ml = parts[k][h];
                 if (ml.y == 0.f) continue;  // no token of the head (NaN scores make it NaN)
-                const float f = exp2f(ml.x - M);
-                den = fmaf(f, ml.y, den);
-                if (f != 0.f) num = fmaf(f, reinterpret_cast<const float *>(rings + k * Ring::BYTES)[i], num);
+                const float f = half_weight(ml.x - M);
+                den = fmaf(f, f * ml.y, den);
+                if (f != 0.f) num = fmaf(f, f * reinterpret_cast<const float *>(rings + k * Ring::BYTES)[i], num);
             }
             const float nan = __int_as_float(0x7fc00000);
             const bool fine = !strange[h], none = den == 0.f;
@@ -874,7 +881,7 @@ template <int D, int CB_NT>
 __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int SUB = CB_NT / D;
-    extern __shared__ float weight[];  // of each share
+    extern __shared__ float weight[];  // of each share, its root
     __shared__ float red[2][CB_NT / 32];
     __shared__ float o_sh[SUB][D];
     const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -897,9 +904,9 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
     float den = 0.f;
     for (int s = threadIdx.x; s < n; s += CB_NT) {
         const float2 ml = __ldcg(&a.part_ml[(slot0 + s) * G + h % G]);
-        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);  // no token of the head (NaN scores make it NaN)
+        const float f = ml.y == 0.f ? 0.f : half_weight(ml.x - M);  // no token of the head (NaN scores make it NaN)
         weight[s] = f;
-        den = fmaf(f, ml.y, den);
+        den = fmaf(f, f * ml.y, den);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(FULL, den, o);
@@ -914,7 +921,7 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
 #pragma unroll 8
     for (int s = sub; s < n; s += SUB) {
         const float f = weight[s], x = __ldcg(p + (size_t)s * G * D);
-        if (f != 0.f) num = fmaf(f, x, num);
+        if (f != 0.f) num = fmaf(f, f * x, num);
     }
     o_sh[sub][j] = num;
     __syncthreads();

@@ -87,3 +87,18 @@ def test_values_without_a_step(value, L):
     out, tau = c.decode(1.0)
     check(c, 1.0, out, tau, sharp=False)
     assert (out - value).abs().max() <= 2.0 ** -18
+
+
+# ------------------------------------------------------------------ references of one head far apart
+
+@gpu
+@pytest.mark.parametrize("L", [900, 5000])
+@pytest.mark.parametrize("power", [40, 60, 90])
+def test_zero_values_beside_large_ones(L, power):
+    """Equal scores, half of the tokens with values of zero, half with values near 2^power (in turn by 16, and by 512):
+    the references of the two differ by more than an exponent of fp32 holds."""
+    for width in (16, 512):
+        half = torch.arange(L) // width % 2 == 0
+        c = Case(1, 4, 1, 64, 16, [L], seed=power, rows=prescribe(torch.zeros(L), half, (~half, 2.0 ** power)))
+        c.write(meta=False)
+        check(c, 1.0, *c.decode(1.0))
