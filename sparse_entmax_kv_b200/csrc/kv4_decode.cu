@@ -53,6 +53,7 @@
 // multiplier (71 -> 77 us); four stages to a ring (no gain);
 // five CTAs an SM (96 registers a thread without spills; scan 121 -> 128 us,
 // softmax of d = 64 82.5 -> 83.2).
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
             for (int v = 0; v < 4; ++v) acc[i][v] = tot[i][v] = 0.f;
         // per column of the lane: the reference (weights are 2^(z - ref)), the
         // sums of p and of p (lo + 8 s) over the lane's tokens
-        float ref[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, off[NG][2] = {};
+        float ref[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, off[NG][2] = {};
         int until = FLUSH;
         for (int i = 0; i < stages; ++i) {
             const int2 *whats;

@@ -102,3 +102,20 @@ def test_zero_values_beside_large_ones(L, power):
         c = Case(1, 4, 1, 64, 16, [L], seed=power, rows=prescribe(torch.zeros(L), half, (~half, 2.0 ** power)))
         c.write(meta=False)
         check(c, 1.0, *c.decode(1.0))
+
+
+# ------------------------------------------------------------------ scores of any size
+
+@gpu
+@pytest.mark.parametrize("L", [1, 900, 5000])
+@pytest.mark.parametrize("score", [-2.0 ** 120, -2.0 ** 101, 2.0 ** 120])
+def test_softmax_of_scores_far_from_zero(L, score):
+    """Tokens of equal scores share the weight evenly, however low (or high) the score is."""
+    c = Case(1, 2, 1, 64, 16, [L], seed=2, rows=prescribe(torch.full((L,), 2.0 ** 50)))
+    c.q[:] = score / 2.0 ** 53
+    c.write(meta=False)
+    out, tau = c.decode(1.0)
+    # equal keys have the same score to the bit, so the weights are 1 / L: sums of L terms and the products' 2^-18
+    V = exact.values(*exact.quantise(f64_of(c.v[:, 0])))
+    assert np.abs(f64_of(out[0]) - V.mean(0)).max() <= 2.0 ** -18 * np.abs(V).max()
+    assert np.abs(f64_of(tau[0]) / score - 1).max() <= 2.0 ** -20
