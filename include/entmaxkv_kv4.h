@@ -13,7 +13,7 @@
  * long.  Every (token, kv head, 64 consecutive coordinates) is quantised by
  * itself, every fl() a rounding to fp32:
  *   lo   = min x                           (a bf16 value)
- *   s    = bf16(fl(fl(max x - lo) * fl(1/15))),  0 when below 2^-126
+ *   s    = bf16(fl(fl(max x - lo) / 15)),  0 when below 2^-126
  *   code = clamp(rint(fl(fl(x - lo) * fl(1 / s))), 0, 15),  0 when s = 0
  * and stands for  value = fl(s * code + lo),  so |value - x| is at most half a
  * step s plus rounding.  A group that holds a NaN or an infinity, or whose

@@ -148,7 +148,7 @@ __device__ __forceinline__ unsigned quantise(const Row16 &row, unsigned (&w)[2])
         w[0] = w[1] = 0u;
         return 0x7fc07fc0u;
     }
-    float s = bf16f(f2bf(__fmul_rn(range, 1.f / 15.f)));
+    float s = bf16f(f2bf(__fdiv_rn(range, 15.f)));
     if (s < 1.17549435e-38f) s = 0.f;  // 2^-126: below, 1 / s may overflow
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
     // s is within 2^-9 of range / 15, so no quotient exceeds 15.04: no clamp

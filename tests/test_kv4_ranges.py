@@ -119,3 +119,68 @@ def test_softmax_of_scores_far_from_zero(L, score):
     V = exact.values(*exact.quantise(f64_of(c.v[:, 0])))
     assert np.abs(f64_of(out[0]) - V.mean(0)).max() <= 2.0 ** -18 * np.abs(V).max()
     assert np.abs(f64_of(tau[0]) / score - 1).max() <= 2.0 ** -20
+
+
+# ------------------------------------------------------------------ the step
+
+def bordering_groups(n, seed=0):
+    """[n, 64] bf16 rows whose range is a whole multiple of 15 away from a border of the step's rounding to bf16:
+    (max - lo) / 15 is halfway between two bf16 values, and a product with a rounded 1/15 need not be."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.empty(n, 64)
+    got = 0
+    while got < n:
+        # 15 (2 m + 1) in units of a half step, and a minimum fine enough to reach it
+        m = int(torch.randint(128, 256, (1,), generator=g))
+        e = int(torch.randint(-12, 4, (1,), generator=g))
+        rng = 15 * (2 * m + 1) * 2.0 ** (e - 1)
+        hi = float(torch.tensor(rng).bfloat16())
+        lo = hi - rng
+        if lo == 0 or float(torch.tensor(lo).bfloat16()) != lo:
+            continue
+        row = lo + (hi - lo) * torch.rand(64, generator=g)
+        row[3], row[40] = lo, hi
+        x[got] = row.bfloat16().float().clamp(lo, hi)
+        got += 1
+    return x
+
+
+def test_bordering_groups_are_on_the_border():
+    x = bordering_groups(200).double().numpy()
+    r = (x.max(-1) - x.min(-1)) / 15
+    assert (exact.f32(r) == r).all()
+    up = exact.bf16(r * (1 + 2.0 ** -20))
+    assert (up != exact.bf16(r * (1 - 2.0 ** -20))).all()
+    by_product = exact.bf16(exact.f32(r * 15 * exact.f32(1 / 15)))
+    assert (by_product != exact.bf16(r)).any()  # the two readings of the step differ on them
+
+
+@gpu
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 64)])
+def test_step_on_a_border(d, P):
+    """Steps that lie halfway between two bf16 values round to even, as the division by 15 says."""
+    n = 300
+    x = bordering_groups(2 * n * d // 64).view(2, n, 1, d)
+    c = Case(1, 1, 1, d, P, [n], rows=lambda k, v: (k.copy_(x[0]), v.copy_(x[1])))
+    c.write()
+    back = [torch.empty(n, 1, d, device="cuda") for _ in range(2)]
+    kv4.entmaxkv_kv4_read(c.shape, c.k4, c.v4, c.start, c.table, c.seq, *back)
+    for rows, got in ((c.k, back[0]), (c.v, back[1])):
+        assert torch.equal(got.cpu().double(), torch.from_numpy(exact.values(*exact.quantise(f64_of(rows)))))
+
+
+@gpu
+@pytest.mark.parametrize("off,scale", [(3.0, 1.0), (0.0, 1.0), (100.0, 0.1), (-20.0, 5.0)])
+def test_rows_with_an_offset_or_an_outlier(off, scale):
+    """Rows read back as the definition has them: offset data, and small rows with one large value a group."""
+    def rows(k, v):
+        k[:] = k * scale + off
+        v *= 0.05
+        v.view(n, 2, 2, 64)[..., 7] = 6.875
+    n = 3000
+    c = Case(1, 2, 2, 128, 32, [n], seed=3, rows=rows)
+    c.write()
+    back = [torch.empty(n, 2, 128, device="cuda") for _ in range(2)]
+    kv4.entmaxkv_kv4_read(c.shape, c.k4, c.v4, c.start, c.table, c.seq, *back)
+    for x, got in ((c.k, back[0]), (c.v, back[1])):
+        assert torch.equal(got.cpu().double(), torch.from_numpy(exact.values(*exact.quantise(f64_of(x)))))
