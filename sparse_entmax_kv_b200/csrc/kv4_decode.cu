@@ -1120,10 +1120,13 @@ constexpr int TK_PASS = 1024;  // listed ones that the CTA takes at a time
 constexpr int TK_BINS = 1024;
 
 // One CTA a head: the candidates above the head's max - 1 in token order, their
-// threshold, and the sum of p v over the support.  Where more are listed than
-// fit on chip, a histogram of them first raises the cut: with every z of a bin
+// threshold, and the sum of p v over the support.  Where more of them are than
+// fit on chip, a histogram first raises the cut: with every z of a bin
 // taken for its lower edge e, the largest edge t with sum (e - t)_+^r >= 1 is
 // below tau (alpha = 1.25 over 120k tokens: 1.7 ms without).
+// What else the shares have listed depends on when they heard of each other's
+// max, so nothing goes by the lists' lengths: the path is chosen by the number
+// above the final cut, and a candidate's thread by its rank among those.
 template <int D, int TK_NT>
 __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
@@ -1176,8 +1179,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const float r = 1.f / (a.alpha - 1.f);
     const int ri = a.r_int;
     float thr = zmax - 1.f;  // nothing at or below it carries weight
-    const float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
-    const unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
+    float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
+    unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
     // listed candidates of a share that reaches the cut
     auto seg_size = [&](int w) {
         const int4 s = __ldcg(seg + (size_t)w * G);
@@ -1202,27 +1205,13 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     const int R = place(seg_size);
     int nc;
     bool onchip = true, bad = false;
-    // every kept candidate, a warp a share: f(place, z, index in the head's list)
+    // the kept candidates, a warp a share, once the lists hold no others:
+    // f(place, index in the head's list)
     auto each = [&](auto f) {
         for (int w = warp; w < W; w += TK_NW) {
-            int at = seg_at[w];
-            if (at == seg_at[w + 1]) continue;
-            const int n = seg_size(w), src = seg_base[w];
-            for (int i0 = 0; i0 < n; i0 += 128) {
-                float z[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + 32 * u + lane;
-                    z[u] = i < n ? __ldcg(zl + src + i) : -INFINITY;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const bool keep = !(z[u] <= thr);
-                    const unsigned bal = __ballot_sync(FULL, keep);
-                    if (keep) f(at + __popc(bal & ((1u << lane) - 1u)), z[u], src + i0 + 32 * u + lane);
-                    at += __popc(bal);
-                }
-            }
+            const int at = seg_at[w], n = seg_at[w + 1] - at, src = seg_base[w];
+#pragma unroll 4
+            for (int i = lane; i < n; i += 32) f(at + i, src + i);
         }
     };
     if (R <= TK_CAP) {
@@ -1284,11 +1273,20 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         int *bins = dyn;
         for (int i = threadIdx.x; i < TK_BINS; i += TK_NT) bins[i] = 0;
         __syncthreads();
-        each([&](int, float z, int) {
-            if (z == z) atomicAdd(&bins[min((int)((z - thr) * TK_BINS), TK_BINS - 1)], 1);
-        });
+        for (int w = warp; w < W; w += TK_NW) {
+            const int n = seg_size(w), src = seg_base[w];
+#pragma unroll 4
+            for (int i = lane; i < n; i += 32) {
+                const float z = __ldcg(zl + src + i);
+                if (z > thr) atomicAdd(&bins[min((int)((z - thr) * TK_BINS), TK_BINS - 1)], 1);
+            }
+        }
+        __syncthreads();
+        int mine = 0, above;
+        for (int i = threadIdx.x; i < TK_BINS; i += TK_NT) mine += bins[i];
+        block_excl_scan(mine, scan, &above);
         int lo = 0;
-        for (int top = TK_BINS - 1; lo < top;) {
+        for (int top = above > TK_CAP ? TK_BINS - 1 : 0; lo < top;) {
             const int mid = (lo + top + 1) >> 1;
             __syncthreads();
             float sum = 0.f;
@@ -1306,28 +1304,46 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         }
         __syncthreads();
         thr = fmaxf(thr, thr + lo * (1.f / TK_BINS) - 1e-6f * fmaxf(1.f, fabsf(zmax)));
-        // how many of each share stay, and where they go
+        // each share's list without what is below the cut; how many stay, and where they go
         for (int w = warp; w < W; w += TK_NW) {
             const int n = seg_size(w);
-            const float *src = zl + seg_base[w];
+            float *zs = zl + seg_base[w];
+            unsigned *rs = rl + seg_base[w];
             int k = 0;
-#pragma unroll 4
-            for (int i = lane; i < n; i += 32) k += !(__ldcg(src + i) <= thr);
+            for (int i0 = 0; i0 < n; i0 += 128) {
+                float z[4];
+                unsigned row[4];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) k += __shfl_xor_sync(FULL, k, o);
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + 32 * u + lane;
+                    z[u] = i < n ? __ldcg(zs + i) : -INFINITY;
+                    row[u] = i < n ? __ldcg(rs + i) : 0u;
+                }
+                __syncwarp();  // the pieces' places are read before any is written over
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const bool keep = !(z[u] <= thr);
+                    const unsigned bal = __ballot_sync(FULL, keep);
+                    bad |= z[u] != z[u];
+                    if (keep) {
+                        const int to = k + __popc(bal & ((1u << lane) - 1u));
+                        zs[to] = z[u];
+                        rs[to] = row[u];
+                    }
+                    k += __popc(bal);
+                }
+            }
             __syncwarp();
             if (lane == 0) seg_at[w] = k;
         }
         __syncthreads();
         nc = place([&](int w) { return seg_at[w]; });
         onchip = nc <= TK_CAP;
-        each([&](int at, float z, int i) {
-            bad |= z != z;
-            if (onchip) {
-                cz[at] = z;
+        if (onchip)
+            each([&](int at, int i) {
+                cz[at] = __ldcg(zl + i);
                 crow[at] = __ldcg(rl + i);
-            }
-        });
+            });
     }
     if (__syncthreads_or(bad)) {
         for (int j = threadIdx.x; j < D; j += TK_NT) a.out[(size_t)bh * D + j] = nan;
@@ -1343,7 +1359,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
                             : entmax_tau_halving<TK_NT>(for_each, thr, hi, r, ri, red);
         };
         if (onchip) tau = solve([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); });
-        else tau = solve([&](auto add, int, int) { each([&](int, float z, int) { add(z); }); });
+        else tau = solve([&](auto add, int, int) { each([&](int, int i) { add(__ldcg(zl + i)); }); });
     }
     if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = tau;
 
@@ -1396,8 +1412,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         for (int i = warp * RPW + sub; i < ns; i += TK_NW * RPW) add_row(cz[i], crow[i]);
     } else {
         for (int w = warp; w < W; w += TK_NW) {
-            if (seg_at[w] == seg_at[w + 1]) continue;
-            const int n = seg_size(w), src = seg_base[w];
+            const int n = seg_at[w + 1] - seg_at[w], src = seg_base[w];
 #pragma unroll 4
             for (int i = sub; i < n; i += RPW) {
                 const float z = __ldcg(zl + src + i);

@@ -184,3 +184,59 @@ def test_rows_with_an_offset_or_an_outlier(off, scale):
     kv4.entmaxkv_kv4_read(c.shape, c.k4, c.v4, c.start, c.table, c.seq, *back)
     for x, got in ((c.k, back[0]), (c.v, back[1])):
         assert torch.equal(got.cpu().double(), torch.from_numpy(exact.values(*exact.quantise(f64_of(x)))))
+
+
+# ------------------------------------------------------------------ the same bits from every call
+
+def rising(L, kept, seed, shares=64):
+    """Scores of which `kept` lie within 1 of the largest (as entmax counts them, alpha 1.5: z = score / 2), in random
+    places, and the rest a little below, so that what a share lists depends on what it has heard of the others."""
+    rng = np.random.RandomState(seed)
+    z = -1.0 - rng.rand(L) * 3.0
+    z[rng.permutation(L)[:kept]] = -rng.rand(kept) * 0.9
+    return torch.from_numpy(z).float()
+
+
+@gpu
+@pytest.mark.parametrize("L,kept", [(60000, 3500), (60000, 4000), (200000, 3000), (60000, 4300)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_listed_candidates_do_not_show(L, kept, d):
+    """The candidates kept are about as many as fit on chip; how many more were listed on the way depends on timing,
+    the result may not.  Other work runs beside the calls."""
+    c = Case(1, 4, 2, d, 32, [L], rows=lambda k, v: k.copy_(2 * rising(L, kept, 5)[:, None, None] / np.sqrt(d)))
+    c.q[:] = 1.0
+    c.q[0, 1], c.q[0, 3] = 1.5, 0.5
+    c.write(meta=False)
+    want = c.decode(1.5)
+    check(c, 1.5, *want, sharp=False)
+    other = torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            with torch.cuda.stream(other):
+                x @ x
+        got = c.decode(1.5)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_supports_beyond_the_chip_do_not_depend_on_the_lists(d):
+    """More tokens with weight than fit on chip, and as many listed that have none."""
+    L = 100000
+    rng = np.random.RandomState(1)
+    z = -0.9 - rng.rand(L)
+    z[rng.permutation(L)[:20000]] = 0.0
+    z[:] += 0.001 * rng.rand(L)
+    c = Case(1, 2, 1, d, 32, [L], rows=lambda k, v: k.copy_(torch.from_numpy(4 * z).float()[:, None, None] / np.sqrt(d)))
+    c.q[:] = 1.0
+    c.write(meta=False)
+    want = c.decode(1.25)
+    other = torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            with torch.cuda.stream(other):
+                x @ x
+        got = c.decode(1.25)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
