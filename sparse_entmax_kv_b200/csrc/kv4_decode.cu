@@ -37,7 +37,8 @@
 //            (z > max so far - 1: no weight exceeds 1) as a list of (z, value
 //            row) for each warp and group; tau_kernel, one CTA a head, drops
 //            those below the head's max - 1, solves for tau and sums p v over
-//            the support
+//            the support.  It counts z from the head's max: the differences
+//            that matter are exact in fp32 and below 1, whatever the scores' size
 //
 // What bounds it: instructions, then memory.  A 16-token tile of 128
 // coordinates (2304 bytes with its values) takes about 400 warp instructions
@@ -942,6 +943,10 @@ __global__ void __launch_bounds__(CB_NT) kv4_combine_kernel(const __grid_constan
 
 // --------------------------------------------------------------- entmax
 
+// What carries no weight beside a largest score m: scores up to m - 1, but
+// never m itself (from 2^24 on, m - 1 may round to m).
+__device__ __forceinline__ float no_weight(float m) { return fminf(m - 1.f, ord2f(f2ord(m) - 1)); }
+
 __global__ void kv4_reset_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     const int G = a.Hq / a.Hkv, i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -1008,7 +1013,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                 if (tm > m[e]) {
                     m[e] = tm;
                     if (a.zmax && tm > known[e] && 2 * c + e < G) atomicMax(a.zmax + h0 + 2 * c + e, f2ord(tm));
-                    thr[e] = fmaxf(thr[e], tm - 1.f);
+                    thr[e] = fmaxf(thr[e], no_weight(tm));
                 }
                 const unsigned lo = __ballot_sync(FULL, !(z[e] <= thr[e])) & column;
                 const unsigned hi = __ballot_sync(FULL, !(z[2 + e] <= thr[e])) & column;
@@ -1041,7 +1046,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
                     if (r == 0 && 2 * c + e < G && m[e] > -INFINITY) atomicMax(a.zmax + h0 + 2 * c + e, f2ord(m[e]));
                     known[e] = ord2f(__ldcg(a.zmax + h0 + (2 * c + e) % G));
                 }
-                thr[e] = fmaxf(m[e], known[e]) - 1.f;
+                thr[e] = no_weight(fmaxf(m[e], known[e]));
             }
             __syncwarp();
 #pragma unroll 1
@@ -1067,7 +1072,7 @@ __global__ void __launch_bounds__(AT_THREADS, SCAN_CTAS) kv4_scan_kernel(const _
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     known[e] = fmaxf(known[e], ord2f(next[e]));
-                    thr[e] = fmaxf(m[e], known[e]) - 1.f;
+                    thr[e] = no_weight(fmaxf(m[e], known[e]));
                     next[e] = __ldcg(a.zmax + h0 + (2 * c + e) % G);
                 }
             }
@@ -1123,7 +1128,8 @@ constexpr int TK_BINS = 1024;
 // threshold, and the sum of p v over the support.  Where more of them are than
 // fit on chip, a histogram first raises the cut: with every z of a bin
 // taken for its lower edge e, the largest edge t with sum (e - t)_+^r >= 1 is
-// below tau (alpha = 1.25 over 120k tokens: 1.7 ms without).
+// below tau (alpha = 1.25 over 120k tokens: 1.7 ms without).  tau and what is
+// held on chip are relative to the head's max: x = z - max in [-1, 0].
 // What else the shares have listed depends on when they heard of each other's
 // max, so nothing goes by the lists' lengths: the path is chosen by the number
 // above the final cut, and a candidate's thread by its rank among those.
@@ -1133,7 +1139,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     constexpr int TK_NW = TK_NT / 32, TK_EACH = TK_PASS / TK_NT;
     constexpr int NG = Kv4<D>::NG;
     extern __shared__ int dyn[];
-    float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates ...
+    float *cz = reinterpret_cast<float *>(dyn);                     // [TK_CAP] the candidates' x ...
     unsigned *crow = reinterpret_cast<unsigned *>(dyn + TK_CAP);    // [TK_CAP] ... and their value rows
     __shared__ float o_sh[TK_NW][D];
     __shared__ float red[2][TK_NW][2];
@@ -1178,7 +1184,9 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 
     const float r = 1.f / (a.alpha - 1.f);
     const int ri = a.r_int;
-    float thr = zmax - 1.f;  // nothing at or below it carries weight
+    const float thr = no_weight(zmax);
+    float cut = -1.f;  // x below it carry no weight
+    auto kept = [&](float z) { return !(z <= thr) && !(z - zmax < cut); };  // NaN stays
     float *zl = a.cand_z + (size_t)bh * a.max_pages * a.P;
     unsigned *rl = a.cand_row + (size_t)bh * a.max_pages * a.P;
     // listed candidates of a share that reaches the cut
@@ -1241,7 +1249,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 #pragma unroll
             for (int u = 0; u < TK_EACH; ++u) {
                 bad |= z[u] != z[u];
-                keep[u] = __ballot_sync(FULL, !(z[u] <= thr));
+                keep[u] = __ballot_sync(FULL, kept(z[u]));
                 if (lane == 0) s_n[u * TK_NW + warp] = __popc(keep[u]);
             }
             __syncthreads();
@@ -1261,8 +1269,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 #pragma unroll
             for (int u = 0; u < TK_EACH; ++u) {
                 const int k = nc + s_n[u * TK_NW + warp] + __popc(keep[u] & ((1u << lane) - 1u));
-                if (!(z[u] <= thr)) {
-                    cz[k] = z[u];
+                if (kept(z[u])) {
+                    cz[k] = z[u] - zmax;
                     crow[k] = row[u];
                 }
             }
@@ -1278,7 +1286,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
 #pragma unroll 4
             for (int i = lane; i < n; i += 32) {
                 const float z = __ldcg(zl + src + i);
-                if (z > thr) atomicAdd(&bins[min((int)((z - thr) * TK_BINS), TK_BINS - 1)], 1);
+                if (z > thr) atomicAdd(&bins[min((int)(fmaxf(z - zmax + 1.f, 0.f) * TK_BINS), TK_BINS - 1)], 1);
             }
         }
         __syncthreads();
@@ -1303,7 +1311,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             else top = mid - 1;
         }
         __syncthreads();
-        thr = fmaxf(thr, thr + lo * (1.f / TK_BINS) - 1e-6f * fmaxf(1.f, fabsf(zmax)));
+        cut = fmaxf(-1.f, lo * (1.f / TK_BINS) - 1.f - 1e-6f);
         // each share's list without what is below the cut; how many stay, and where they go
         for (int w = warp; w < W; w += TK_NW) {
             const int n = seg_size(w);
@@ -1322,7 +1330,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
                 __syncwarp();  // the pieces' places are read before any is written over
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const bool keep = !(z[u] <= thr);
+                    const bool keep = kept(z[u]);
                     const unsigned bal = __ballot_sync(FULL, keep);
                     bad |= z[u] != z[u];
                     if (keep) {
@@ -1341,7 +1349,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         onchip = nc <= TK_CAP;
         if (onchip)
             each([&](int at, int i) {
-                cz[at] = __ldcg(zl + i);
+                cz[at] = __ldcg(zl + i) - zmax;
                 crow[at] = __ldcg(rl + i);
             });
     }
@@ -1350,18 +1358,18 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = nan;
         return;
     }
-    const float hi = zmax - powf((float)nc, 1.f - a.alpha);
-    float tau = thr;
-    if (nc > 1 && hi > thr) {
+    const float hi = -powf((float)nc, 1.f - a.alpha);
+    float tau = cut;
+    if (nc > 1 && hi > cut) {
         // off chip every thread adds the candidates of its place, pass by pass
         auto solve = [&](auto for_each) {
-            return r >= 1.f ? entmax_tau<TK_NT>(for_each, nc, thr, hi, zmax, r, ri, red)
-                            : entmax_tau_halving<TK_NT>(for_each, thr, hi, r, ri, red);
+            return r >= 1.f ? entmax_tau<TK_NT>(for_each, nc, cut, hi, 0.f, r, ri, red)
+                            : entmax_tau_halving<TK_NT>(for_each, cut, hi, r, ri, red);
         };
         if (onchip) tau = solve([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); });
-        else tau = solve([&](auto add, int, int) { each([&](int, int i) { add(__ldcg(zl + i)); }); });
+        else tau = solve([&](auto add, int, int) { each([&](int, int i) { add(__ldcg(zl + i) - zmax); }); });
     }
-    if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = tau;
+    if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = zmax + tau;
 
     // p v over the support.  A value word holds 4 coordinates of both tokens
     // of a pair: one word a lane is a row (d = 128), half a warp a row (64).
@@ -1415,8 +1423,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             const int n = seg_at[w + 1] - seg_at[w], src = seg_base[w];
 #pragma unroll 4
             for (int i = sub; i < n; i += RPW) {
-                const float z = __ldcg(zl + src + i);
-                const float p = pos_pow(z - tau, r, ri);
+                const float p = pos_pow(__ldcg(zl + src + i) - zmax - tau, r, ri);
                 if (p > 0.f) add_row(p, __ldcg(rl + src + i));
             }
         }

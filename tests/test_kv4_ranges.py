@@ -240,3 +240,37 @@ def test_supports_beyond_the_chip_do_not_depend_on_the_lists(d):
                 x @ x
         got = c.decode(1.25)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.25, 1.5, 2.0, 3.0])
+@pytest.mark.parametrize("score", [2.0 ** 23, 2.0 ** 25, -2.0 ** 26, 1e8, -1e8, 1e12, -2.0 ** 120])
+def test_entmax_of_scores_far_from_zero(alpha, score):
+    """The largest token carries weight however large its score is: one alone, or several alike."""
+    for L, top in ((1, [0]), (700, [345]), (700, [3, 44, 699]), (30000, [12345, 23000])):
+        a = torch.full((L,), 1.0 if score < 0 else 0.5)
+        a[top] = 0.75 if score < 0 else 1.0
+        c = Case(1, 2, 1, 64, 16, [L], seed=len(top), rows=prescribe(a * 2.0 ** 30))
+        c.q[:] = score / 8 / 2.0 ** 30
+        c.write(meta=False)
+        out, tau = c.decode(alpha)
+        V = exact.values(*exact.quantise(f64_of(c.v[:, 0])))[top]
+        # z is the same to the bit for equal keys, so the weights are equal: (1 / n)
+        assert np.abs(f64_of(out[0]) - V.mean(0)).max() <= 2.0 ** -19 * np.abs(V).max(), (L, top)
+        z = (alpha - 1) * float(c.q[0, 0, 0]) * 8 * float(a[top[0]]) * 2.0 ** 30
+        assert np.abs(f64_of(tau[0]) - (z - len(top) ** (1 - alpha))).max() <= 2.0 ** -21 * abs(z), (L, top)
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.25, 1.5, 2.0])
+@pytest.mark.parametrize("offset", [0.0, 20.0, -180.0])
+def test_entmax_weights_do_not_feel_a_common_offset(alpha, offset):
+    """A common offset of the scores leaves the weights: tau is solved below the largest z, so what is lost is each
+    score's own rounding.  The first 64 coordinates hold the offset, the others what tells the tokens apart."""
+    def rows(k, v):
+        k[..., :64] = offset
+        k[..., 64:] = (torch.randint(0, 24, (k.shape[0],), generator=torch.Generator().manual_seed(6)) / 64)[:, None, None]
+    c = Case(1, 2, 1, 128, 16, [600], seed=6, rows=rows)
+    c.q[:] = 1.0
+    c.write(meta=False)
+    check(c, alpha, *c.decode(alpha))
