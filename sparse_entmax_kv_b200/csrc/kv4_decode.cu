@@ -22,7 +22,10 @@
 //           of the largest (values below 2^-86 get less).  Groups of four heads or fewer put the two parts
 //           in the columns their heads leave free.  The sums move to a second
 //           set of fp32 registers every few tiles, so that few truncations
-//           meet a large sum.
+//           meet a large sum.  With eight heads the lower parts would be
+//           truncated against the sum of the upper ones, product by product
+//           (124k tokens: 2.7e-6 off instead of 4e-7): there each tile begins at
+//           zero with the lower parts, and its sums move at once
 //
 // The chunks (16 or 32 tokens of one kv head) of all groups' page lists form one
 // range that is cut evenly among the warps of a grid that fills the GPU once:
@@ -439,6 +442,15 @@ __device__ __forceinline__ unsigned transpose8(unsigned x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// D = A(16x16 fp16, row) * B(16x8 fp16, col), fp32 sums.
+__device__ __forceinline__ void mul_f16_16816(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3,
+                                              unsigned b0, unsigned b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + D, fp32 sums.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3,
                                               unsigned b0, unsigned b1) {
@@ -613,8 +625,8 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
     kv4_softmax_kernel(const __grid_constant__ Kv4DecodeArgs a) {
     pdl_wait();
     constexpr int NG = Kv4<D>::NG, WPL = Kv4<D>::WPL, MT = D / 16, NE = Queries<D, G>::NE;
-    constexpr int NB = G == 8 ? 2 : 1;  // products per value operand: both parts, or both in one
-    constexpr int FLUSH = 8 / NB;       // tiles between flushes of the output sums
+    constexpr bool APART = G == 8;  // two products per value operand, one for each part (else one for both)
+    constexpr int FLUSH = 8;        // tiles between flushes of the output sums (APART: one)
     using Ring = TileRing<D, true>;
     extern __shared__ __align__(128) unsigned char rings[];
     __shared__ uint64_t bars[WARPS][RING_STAGES];
@@ -739,7 +751,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                         for (int k = 0; k < MT; ++k)
 #pragma unroll
                             for (int v = 0; v < 4; ++v) {
-                                acc[k][v] *= corr[v & 1];
+                                if (!APART) acc[k][v] *= corr[v & 1];
                                 tot[k][v] *= corr[v & 1];
                             }
                         weights(Yes{});
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         // token by column, to column by token
-                        unsigned bf[NB][2];
+                        unsigned bf[APART ? 2 : 1][2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const float x0 = x[g][2 * u], x1 = x[g][2 * u + NE - 1];
@@ -772,20 +784,28 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                                 bf[0][u] = transpose8(rest ? lo : hi);
                             }
                         }
+                        auto sums = [&](int i, unsigned c0, unsigned c1, unsigned c2, unsigned c3) {
+                            if constexpr (APART) {
+                                float t[4];
+                                mul_f16_16816(t, c0, c1, c2, c3, bf[1][0], bf[1][1]);
+                                mma_f16_16816(t, c0, c1, c2, c3, bf[0][0], bf[0][1]);
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) tot[i][v] += t[v];
+                            } else {
+                                mma_f16_16816(acc[i], c0, c1, c2, c3, bf[0][0], bf[0][1]);
+                            }
+                        };
 #pragma unroll
                         for (int k = 2 * g; k < 2 * g + 2; ++k) {
                             const unsigned a0 = code_f16<0>(w0[k], one), a1 = code_f16<1>(w0[k], one),
                                            a2 = code_f16<0>(w1[k], one), a3 = code_f16<1>(w1[k], one);
-#pragma unroll
-                            for (int q = 0; q < NB; ++q) mma_f16_16816(acc[2 * k], a0, a1, a2, a3, bf[q][0], bf[q][1]);
+                            sums(2 * k, a0, a1, a2, a3);
                             const unsigned d0 = code_f16<2>(w0[k], one), d1 = code_f16<3>(w0[k], one),
                                            d2 = code_f16<2>(w1[k], one), d3 = code_f16<3>(w1[k], one);
-#pragma unroll
-                            for (int q = 0; q < NB; ++q)
-                                mma_f16_16816(acc[2 * k + 1], d0, d1, d2, d3, bf[q][0], bf[q][1]);
+                            sums(2 * k + 1, d0, d1, d2, d3);
                         }
                     }
-                    if (--until == 0) {
+                    if (!APART && --until == 0) {
                         until = FLUSH;
 #pragma unroll
                         for (int k = 0; k < MT; ++k)
@@ -823,7 +843,8 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
             // tile k holds coordinates j (row r) and j + 1 (row r + 8)
             const int j = 64 * (k >> 2) + 8 * r + 4 * ((k >> 1) & 1) + 2 * (k & 1);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) tot[k][v] += acc[k][v];
+            for (int v = 0; v < 4; ++v)
+                if (!APART) tot[k][v] += acc[k][v];
 #pragma unroll
             for (int v = 0; v < 4; v += G == 1 ? 2 : 1) {
                 float o = tot[k][v];

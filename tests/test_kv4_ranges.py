@@ -274,3 +274,25 @@ def test_entmax_weights_do_not_feel_a_common_offset(alpha, offset):
     c.q[:] = 1.0
     c.write(meta=False)
     check(c, alpha, *c.decode(alpha))
+
+
+# ------------------------------------------------------------------ eight heads a group
+
+@gpu
+@pytest.mark.parametrize("d,P", [(64, 32), (128, 16)])
+def test_eight_heads_are_as_exact_as_four(d, P):
+    """Long softmax of eight heads that share their keys: no further from 64 bits than the same heads in groups of
+    four over the same cache (their weights take other columns of the products, and the same two parts)."""
+    c = Case(1, 8, 1, d, P, [60000], seed=11)
+    c.write(meta=False)
+    out = f64_of(c.decode(1.0)[0])
+    want = np.stack([head_of(c, 0, h, 1.0)[0] for h in range(8)])
+    off = np.linalg.norm(out[0] - want) / np.linalg.norm(want)
+    four = nv.Shape(1, 4, 1, d, P, c.mp, c.shape.num_blocks)
+    parts, q = [], c.q
+    for h in (0, 4):
+        c.q = q[:, h:h + 4].contiguous()
+        got = torch.empty(1, 4, d, device="cuda")
+        parts.append(f64_of(c.decode(1.0, shape=four, out=got, tau=torch.empty(1, 4, device="cuda"))[0])[0])
+    ref_off = np.linalg.norm(np.concatenate(parts) - want) / np.linalg.norm(want)
+    assert off <= 2 * ref_off + 2.0 ** -24, (off, ref_off)
