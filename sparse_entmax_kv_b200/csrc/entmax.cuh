@@ -86,28 +86,58 @@ __device__ float entmax_tau(ForEach for_each, int n, float lo, float hi, float z
     return t;
 }
 
-// The same root by halving [lo, hi], for any r > 0.  With r < 1 a token that
-// comes into the support does so with an infinite slope, and Newton's steps
-// may pass the root back and forth.
-template <int NT, class ForEach>
-__device__ float entmax_tau_halving(ForEach for_each, float lo, float hi, float r, int ri, float (*red)[NT / 32][2]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int it = 0; it < 40; ++it) {
-        const float mid = 0.5f * (lo + hi);
-        if (!(mid > lo && mid < hi)) break;  // neighbours
-        float s = 0.f;
-        for_each([&](float z) { s += pos_pow(z - mid, r, ri); }, (int)threadIdx.x, NT);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-        if (lane == 0) red[it & 1][warp][0] = s;
-        __syncthreads();
-        s = 0.f;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) s += red[it & 1][w][0];
-        if (s >= 1.f) lo = mid;
-        else hi = mid;
+// The same root for r < 1, by halving [lo, hi]: a token that comes into the
+// support does so with an infinite slope, and Newton's steps may pass the root
+// back and forth.  The weight of a token next to the root hangs on more bits
+// of z - t than there are (alpha = 10: a weight of 0.1 is z - t = 1e-9, one of
+// 0.03 2e-14), but is well determined by the others': tokens between the
+// neighbours lo and hi that the halving (in 64 bits) ends with share what those
+// above hi leave.
+struct EntmaxEdge {
+    double lo = 0., hi = 0.;  // sum [z - lo]_+^r >= 1, sum [z - hi]_+^r <= 1
+    float rest = 0.f;         // weight of each token in (lo, hi]
+    __device__ __forceinline__ float weight(float z, float r) const {
+        return (double)z > hi ? powf((float)((double)z - hi), r) : (double)z > lo ? rest : 0.f;
     }
-    return lo;
+};
+template <int NT, class ForEach>
+__device__ EntmaxEdge entmax_tau_halving(ForEach for_each, float from, float to, float r, float (*red)[NT / 32][2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    EntmaxEdge e;
+    e.lo = from;
+    e.hi = to;
+    for (int it = 0;; ++it) {
+        const double mid = 0.5 * (e.lo + e.hi);
+        const bool last = it == 80 || !(mid > e.lo && mid < e.hi);  // neighbours, or both next to 0
+        const double t = last ? e.hi : mid;
+        float s = 0.f, n = 0.f;
+        for_each([&](float z) {
+            if ((double)z > t) s += powf((float)((double)z - t), r);
+            else if (last && (double)z > e.lo) n += 1.f;
+        }, (int)threadIdx.x, NT);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            s += __shfl_xor_sync(FULL, s, o);
+            n += __shfl_xor_sync(FULL, n, o);
+        }
+        if (lane == 0) {
+            red[it & 1][warp][0] = s;
+            red[it & 1][warp][1] = n;
+        }
+        __syncthreads();
+        s = n = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            s += red[it & 1][w][0];
+            n += red[it & 1][w][1];
+        }
+        if (last) {
+            e.rest = n > 0.f ? fmaxf(1.f - s, 0.f) / n : 0.f;
+            return e;
+        }
+        if (s >= 1.f) e.lo = mid;
+        else e.hi = mid;
+    }
 }
 
 }  // namespace ekv

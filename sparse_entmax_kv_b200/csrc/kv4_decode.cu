@@ -1381,16 +1381,23 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     }
     const float hi = -powf((float)nc, 1.f - a.alpha);
     float tau = cut;
+    EntmaxEdge edge;  // alpha > 2
+    edge.lo = edge.hi = cut;
     if (nc > 1 && hi > cut) {
         // off chip every thread adds the candidates of its place, pass by pass
         auto solve = [&](auto for_each) {
-            return r >= 1.f ? entmax_tau<TK_NT>(for_each, nc, cut, hi, 0.f, r, ri, red)
-                            : entmax_tau_halving<TK_NT>(for_each, cut, hi, r, ri, red);
+            if (r >= 1.f) {
+                tau = entmax_tau<TK_NT>(for_each, nc, cut, hi, 0.f, r, ri, red);
+            } else {
+                edge = entmax_tau_halving<TK_NT>(for_each, cut, hi, r, red);
+                tau = (float)edge.lo;
+            }
         };
-        if (onchip) tau = solve([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); });
-        else tau = solve([&](auto add, int, int) { each([&](int, int i) { add(__ldcg(zl + i) - zmax); }); });
+        if (onchip) solve([&](auto add, int f, int st) { for (int i = f; i < nc; i += st) add(cz[i]); });
+        else solve([&](auto add, int, int) { each([&](int, int i) { add(__ldcg(zl + i) - zmax); }); });
     }
     if (threadIdx.x == 0 && a.tau_out) a.tau_out[bh] = zmax + tau;
+    auto weight = [&](float x) { return r >= 1.f ? pos_pow(x - tau, r, ri) : edge.weight(x, r); };
 
     // p v over the support.  A value word holds 4 coordinates of both tokens
     // of a pair: one word a lane is a row (d = 128), half a warp a row (64).
@@ -1419,7 +1426,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
         int ns = 0;
         for (int i0 = 0; i0 < nc; i0 += TK_NT) {
             const int i = i0 + threadIdx.x;
-            const float p = i < nc ? pos_pow(cz[i] - tau, r, ri) : 0.f;
+            const float p = i < nc ? weight(cz[i]) : 0.f;
             const unsigned row = i < nc ? crow[i] : 0u;
             const unsigned keep = __ballot_sync(FULL, p > 0.f);
             if (lane == 0) s_n[warp] = __popc(keep);
@@ -1444,7 +1451,7 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
             const int n = seg_at[w + 1] - seg_at[w], src = seg_base[w];
 #pragma unroll 4
             for (int i = sub; i < n; i += RPW) {
-                const float p = pos_pow(__ldcg(zl + src + i) - zmax - tau, r, ri);
+                const float p = weight(__ldcg(zl + src + i) - zmax);
                 if (p > 0.f) add_row(p, __ldcg(rl + src + i));
             }
         }

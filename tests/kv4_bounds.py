@@ -56,9 +56,11 @@ def attention(q, keys, vals, alpha):
     """One head: q [d], keys and vals (codes, s, lo) of its tokens -> out, tau (or log-sum-exp), and the bounds of both.
 
     Weights move with the scores.  Softmax: each by a factor of at most exp(2 max dz).  Entmax: tau moves by at most
-    the largest dz, so x = z - tau by twice that (and by 2^-21 for its own fp32 steps and the solver's tolerance);
-    powers, sums and the division add 2^-18 of the terms' size.  Only tokens that can have weight count, so the bound
-    is far below the output itself.
+    the largest dz, so x = z - tau by twice that; weights of moved scores still sum to 1, so what each adds is its
+    move times |v - o|.  The solver's tau, and z and tau as fp32 counted from the largest z, put each x off by
+    another 2^-23 + 3 * 2^-25 < 2^-22, after which the sum may not be 1: those moves count times |v|.  (Above alpha =
+    2 a token next to tau gets what the others leave, and the sum is 1.)  Powers, sums and the division add 2^-18 of
+    the terms' size.  Only tokens that can have weight count, so the bound is far below the output itself.
     """
     d = q.shape[0]
     scale = (alpha - 1 if alpha > 1 else 1.0) / np.sqrt(d)
@@ -71,7 +73,7 @@ def attention(q, keys, vals, alpha):
         p = np.exp(z - top)
         tau = top + np.log(p.sum())
         p /= p.sum()
-        moved = p * np.expm1(np.minimum(2 * dz[p > 2.0 ** -60].max(), 1.0))
+        moved, loose = p * np.expm1(np.minimum(2 * dz[p > 2.0 ** -60].max(), 1.0)), 0 * p
     else:
         r, x = 1 / (alpha - 1), z - top
         a, b = -1.0, 0.0
@@ -79,9 +81,15 @@ def attention(q, keys, vals, alpha):
             mid = (a + b) / 2
             a, b = (mid, b) if (np.maximum(x - mid, 0) ** r).sum() >= 1 else (a, mid)
         p = np.maximum(x - a, 0) ** r
+        edge = (x > a) & (x <= b)  # more bits than there are tell x from tau: what the others leave
+        if r < 1 and edge.any():
+            p = np.where(x > b, np.maximum(x - b, 0) ** r, 0)
+            p[edge] = (1 - p.sum()) / edge.sum()
         tau = top + a
         near = x - a > -2.0 ** -8
-        moved = _rise(x - a, 2 * dz[near].max() + 2.0 ** -21, r)
+        e = 2 * dz[near].max()
+        moved = _rise(x - a, e, r)
+        loose = _rise(x - a, e + 2.0 ** -22, r) - moved if r >= 1 else 0 * p
     o = p @ V
-    do = moved @ np.abs(V - o) + 2.0 ** -18 * (p @ size) + 2.0 ** -126
+    do = moved @ np.abs(V - o) + loose @ np.abs(V) + 2.0 ** -18 * (p @ size) + 2.0 ** -126
     return o, tau, do, dz[p > 2.0 ** -60].max() + 2.0 ** -21 + 2.0 ** -22 * abs(tau)

@@ -296,3 +296,98 @@ def test_eight_heads_are_as_exact_as_four(d, P):
         parts.append(f64_of(c.decode(1.0, shape=four, out=got, tau=torch.empty(1, 4, device="cuda"))[0])[0])
     ref_off = np.linalg.norm(np.concatenate(parts) - want) / np.linalg.norm(want)
     assert off <= 2 * ref_off + 2.0 ** -24, (off, ref_off)
+
+
+# ------------------------------------------------------------------ alpha > 2: tokens next to the threshold
+
+@gpu
+@pytest.mark.parametrize("alpha", [3.0, 5.0, 10.0, 100.0, 1000.0])
+@pytest.mark.parametrize("gap", [0.01, 0.35, 0.9])
+@pytest.mark.parametrize("n", [1, 3, 5000])
+def test_weight_next_to_the_threshold(alpha, gap, n):
+    """One token above n equal ones (and others without weight): theirs is p with n p + (gap + p^(alpha-1))^r = 1, where
+    gap + p^(alpha-1) is the first one's distance from tau, which in fp32 is no longer told from gap."""
+    L, d = n + 40, 64
+    # z = (alpha - 1) 8 k: the first token's, the n equal ones', and what lies 3 below
+    k = np.full(L, -3.0)
+    k[17], k[30:30 + n] = 0.0, -gap
+    c = Case(1, 1, 1, d, 16, [L], seed=n, rows=prescribe(torch.from_numpy(k).float()))
+    c.q[:] = 1 / (8 * (alpha - 1))
+    c.write(meta=False)
+    out, tau = c.decode(alpha)
+    z = (alpha - 1) * f64_of(c.k[:, 0, 0]) * float(c.q[0, 0, 0]) * 8
+    r, gap = 1 / (alpha - 1), z[17] - z[30]
+    a, b = 0.0, 1.0 / n
+    for _ in range(200):
+        p = (a + b) / 2
+        a, b = (p, b) if n * p + (gap + p ** (alpha - 1)) ** r < 1 else (a, p)
+    codes, s, lo = exact.quantise(f64_of(c.v[:, 0]))
+    V = exact.values(codes, s, lo)
+    want = (1 - n * p) * V[17] + p * V[30:30 + n].sum(0)
+    # dz < 2^-20 (scores below 4): the first weight moves by r gap^(r - 1) 2 dz < 2^-12 at gap = 0.01 and by less
+    # above, and the others' sum by as much the other way; powers and sums add 2^-18 of their terms.  A term is the
+    # sum of p s c and p lo, each rounded by itself, so its size is p (15 s + |lo|), not p |v|
+    first, others = V[17], V[30:30 + n].mean(0)
+    size = np.repeat(15 * s + np.abs(lo), 64, -1)
+    tol = r * gap ** (r - 1) * 2.0 ** -19 * np.abs(first - others)
+    tol = tol + 2.0 ** -18 * ((1 - n * p) * size[17] + p * size[30:30 + n].sum(0))
+    assert (np.abs(f64_of(out[0, 0]) - want) <= tol).all()
+    assert abs(float(tau[0, 0]) - (z[30] - p ** (alpha - 1))) <= 2.0 ** -18
+
+
+# ------------------------------------------------------------------ outputs held to sharp bounds
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.25, 1.5, 1.7, 2.0, 3.0, 10.0, 1000.0])
+@pytest.mark.parametrize("G,Hkv,d,P", [(1, 3, 64, 16), (2, 1, 128, 32), (4, 2, 128, 16), (8, 1, 64, 64)])
+def test_outputs_to_sharp_bounds(alpha, G, Hkv, d, P):
+    """Every head within bounds that an output of zeros, or with its coordinates moved on by one, breaks."""
+    c = Case(3, G * Hkv, Hkv, d, P, [1, P - 1, 700], seed=int(alpha * 10) + G)
+    c.write(meta=False)
+    check(c, alpha, *c.decode(alpha))
+    assert nv.get_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("alpha", [1.0, 1.25, 1.5, 2.0, 3.0, 30.0])
+@pytest.mark.parametrize("G,d,P", [(1, 64, 32), (4, 128, 16)])
+def test_kept_pages_to_sharp_bounds(alpha, G, d, P):
+    c = Case(1, 2 * G, 2, d, P, [900], seed=8)
+    c.write()
+    n = -(-900 // P)
+    rng = np.random.RandomState(2)
+    sel = np.full((1, c.Hq, c.mp), -9, np.int32)
+    picks = [np.sort(rng.choice(n, 9, False)) for _ in range(c.Hq)]
+    for h, p in enumerate(picks):
+        sel[0, h, :9] = p
+    out, tau = c.decode(alpha, torch.from_numpy(sel).cuda(), torch.full((1, c.Hq), 9, dtype=torch.int32, device="cuda"))
+    out, tau = f64_of(out), f64_of(tau)
+    for h, p in enumerate(picks):
+        tok = (p[:, None] * P + np.arange(P)).reshape(-1)
+        o, t, do, dt = head_of(c, 0, h, alpha, tok[tok < 900])
+        assert (np.abs(out[0, h] - o) <= do).all(), (h, np.abs(out[0, h] - o).max(), do.max())
+        assert abs(tau[0, h] - t) <= dt and (np.abs(o) > 4 * do).any()
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5, 2.0, 3.0, 10.0, 1000.0])
+def test_the_bounds_are_sharp(alpha):
+    """Without a GPU: an fp32 evaluation meets the bounds; zeros, another order of the coordinates, the uniform mean
+    and the output of softmax (for entmax) or of entmax (for softmax) do not."""
+    rng = np.random.RandomState(int(alpha))
+    q, K, V = rng.randn(128), rng.randn(700, 128), rng.randn(700, 128)
+    q, K, V = (exact.bf16(x) for x in (q, K, V))
+    k, v = exact.quantise(K), exact.quantise(V)
+    o, t, do, dt = exact.attention(q, k, v, alpha)
+    Kf, Vf, qf = (np.asarray(x, np.float32) for x in (exact.values(*k), exact.values(*v), q))
+    z = Kf @ qf * np.float32((alpha - 1 if alpha > 1 else 1) / np.sqrt(128))
+    if alpha == 1:
+        w = np.exp(z - z.max())
+        w /= w.sum()
+    else:
+        w = np.maximum(z - np.float32(t), 0) ** np.float32(1 / (alpha - 1))
+    near = w @ Vf
+    assert (np.abs(near - o) <= do).all()
+    other = exact.attention(q, k, v, 1.0 if alpha > 1 else 1.5)[0]
+    for wrong in (0 * o, np.roll(o, 1), exact.values(*v).mean(0), other):
+        assert (np.abs(wrong - o) > do).any()
+    assert (np.abs(o) > 4 * do).any() and dt < 1e-3 * max(1, alpha - 1)
