@@ -58,8 +58,9 @@ ENTMAXKV_API int entmaxkv_pages_refs(const entmaxkv_shape *shape, const int32_t 
 /*
  * Row b of the new table continues row parent[b] of the old one (int32 [B];
  * -1: an empty row, its sequence is freed).  lens_out[b] =
- * lens_in[parent[b]]; full pages are shared; of the rows with the same
- * parent the first keeps a partial last page and each other one gets a copy
+ * lens_in[parent[b]]; full pages are shared.  Of the rows with the same
+ * parent p, row p itself keeps a partial last page if it is among them
+ * (parent[p] == p), else the first of them; each other one gets a copy
  * of it in a new block (the free blocks of the OLD table, in ascending order
  * of b), in every buffer of bufs.  Entries past a row's pages become -1.
  * When the free blocks run out, the rows left over lose their partial page
