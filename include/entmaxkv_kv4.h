@@ -104,7 +104,10 @@ ENTMAXKV_API size_t entmaxkv_kv4_workspace_size(const entmaxkv_shape *shape);
  * pinned host memory), tau_out fp32 [B][Hq].  Scores are held in fp32 in the
  * units of a query whose largest coordinate is near 2^13, softmax weights in
  * units of the values' steps: beyond magnitudes of 2^100, keys may overflow
- * and values lose their smallest weights.  A head without tokens gets
+ * and values lose their smallest weights.  Near alpha = 1 entmax weights are
+ * powers of 1/(alpha - 1) > 100, which the rounding of z - tau is multiplied
+ * by: out is off by 5e-6 (relative) at alpha = 1.01, 5e-5 at 1.001 and 6e-4 at
+ * 1.0001.  A head without tokens gets
  * out = 0, tau = NaN; a non-finite query row NaN, and
  * ENTMAXKV_STATUS_NONFINITE.  NaN values that carry weight, and NaN keys,
  * make out NaN.  Results do not depend on the order in which CTAs run.

@@ -44,11 +44,11 @@
 //            that matter are exact in fp32 and below 1, whatever the scores' size
 //
 // What bounds it: instructions, then memory.  A 16-token tile of 128
-// coordinates (2304 bytes with its values) takes about 400 warp instructions
-// with its values and 242 without, most of them to make operands of codes; the
-// integer pipe is 45 to 48 % busy, the issue slots 60 to 65 %, the tensor
+// coordinates (2304 bytes with its values) takes about 403 warp instructions
+// with its values and 244 without, most of them to make operands of codes; the
+// integer pipe is 44 to 48 % busy, the issue slots 60 to 65 %, the tensor
 // pipe 16 to 20 %.  Softmax over 8 sequences of 16k to 32k tokens, 8 kv heads of 4,
-// d = 128: 68 us, 236 MB at 3.5 TB/s (53 % of a copy's rate); entmax over 4
+// d = 128: 69 us, 236 MB at 3.4 TB/s (52 % of a copy's rate); entmax over 4
 // of 64k to 128k: 117 us, of which the scan is 100 (271 MB at 2.7 TB/s).
 // Tried and dropped: units of a quarter of a warp's share, taken from a queue
 // in one CTA an SM (71 -> 84 us, 126 -> 145: each pays for its queries and its
@@ -460,6 +460,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsign
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Off by 2^-22 of the result at most, as much as the weight's two fp16 parts leave.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1405,6 +1406,8 @@ __global__ void __launch_bounds__(TK_NT) kv4_tau_kernel(const __grid_constant__ 
     constexpr int RPW = 32 / LPR;     // rows of a warp at a time
     const int ll = lane % LPR, sub = lane / LPR;
     const int piece = ll / Kv4<D>::WPL, wi = ll % Kv4<D>::WPL;
+    // In fp32: a warp adds its share of a support that is mostly a few dozen tokens,
+    // and outputs are 3 to 6e-7 off with it, as far as the scores' own rounding puts them.
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const size_t block = (size_t)(a.P / 16) * Kv4<D>::TILE;
     auto add_row = [&](float p, unsigned row) {
