@@ -60,14 +60,16 @@ def attention(q, keys, vals, alpha):
     move times |v - o|.  The solver's tau, and z and tau as fp32 counted from the largest z, put each x off by
     another 2^-23 + 3 * 2^-25 < 2^-22, after which the sum may not be 1: those moves count times |v|.  (Above alpha =
     2 a token next to tau gets what the others leave, and the sum is 1.)  Powers, sums and the division add 2^-18 of
-    the terms' size.  Only tokens that can have weight count, so the bound is far below the output itself.
+    the terms' size: of p s c and p lo (entmax) or p s (c - 8) and p (lo + 8 s) (softmax), which may cancel in a value
+    near zero, so 16 s + |lo| is taken for either.  Only tokens that can have weight count, so the bound is far
+    below the output itself.
     """
     d = q.shape[0]
     scale = (alpha - 1 if alpha > 1 else 1.0) / np.sqrt(d)
     z, dz = _scores(q, keys, scale)
     c, s, lo = vals
     V = values(c, s, lo)
-    size = _spread(s) * np.abs(c - 8) + _spread(np.abs(lo + 8 * s))
+    size = _spread(16 * s + np.abs(lo))
     top = z.max()
     if alpha == 1:
         p = np.exp(z - top)

@@ -243,6 +243,34 @@ def test_supports_beyond_the_chip_do_not_depend_on_the_lists(d):
 
 
 @gpu
+@pytest.mark.parametrize("at", [777, 50000])
+@pytest.mark.parametrize("kept,extra,alpha", [(3500, 1500, 1.5), (3500, 3000, 1.5), (20000, 80000, 1.25)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_score_above_the_rest_is_heard_of_late(d, kept, extra, alpha, at):
+    """One token 0.5 above the others: until a share hears of it, it lists `extra` tokens that carry no weight beside
+    it, in numbers that change from call to call, around what fits on chip (4096) and far beyond it."""
+    L = 100000
+    rng = np.random.RandomState(1)
+    z, p = -2.0 - rng.rand(L), rng.permutation(L)
+    z[p[:kept]] = -(0.49 if kept < 4096 else 0.001) * rng.rand(kept)
+    z[p[kept:kept + extra]] = -0.55 - 0.4 * rng.rand(extra)
+    z[at] = 0.5
+    c = Case(1, 2, 1, d, 32, [L], rows=prescribe(torch.from_numpy(z / (alpha - 1)).float() / np.sqrt(d)))
+    c.q[:] = 1.0
+    c.write(meta=False)
+    want = c.decode(alpha)
+    check(c, alpha, *want, sharp=False)
+    other = torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            with torch.cuda.stream(other):
+                x @ x
+        got = c.decode(alpha)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+
+
+@gpu
 @pytest.mark.parametrize("alpha", [1.25, 1.5, 2.0, 3.0])
 @pytest.mark.parametrize("score", [2.0 ** 23, 2.0 ** 25, -2.0 ** 26, 1e8, -1e8, 1e12, -2.0 ** 120])
 def test_entmax_of_scores_far_from_zero(alpha, score):
