@@ -24,8 +24,8 @@
 //           set of fp32 registers every few tiles, so that few truncations
 //           meet a large sum.  With eight heads the lower parts would be
 //           truncated against the sum of the upper ones, product by product
-//           (124k tokens: 2.7e-6 off instead of 4e-7): there each tile begins at
-//           zero with the lower parts, and its sums move at once
+//           (124k tokens: 2.7e-6 off instead of 3.4e-7): there the products of
+//           each tile and part begin at zero and move at once
 //
 // The chunks (16 or 32 tokens of one kv head) of all groups' page lists form one
 // range that is cut evenly among the warps of a grid that fills the GPU once:
@@ -787,11 +787,13 @@ __global__ void __launch_bounds__(32 * WARPS, (WHOLE ? 1 : softmax_ctas<D, G>())
                         }
                         auto sums = [&](int i, unsigned c0, unsigned c1, unsigned c2, unsigned c3) {
                             if constexpr (APART) {
-                                float t[4];
-                                mul_f16_16816(t, c0, c1, c2, c3, bf[1][0], bf[1][1]);
-                                mma_f16_16816(t, c0, c1, c2, c3, bf[0][0], bf[0][1]);
 #pragma unroll
-                                for (int v = 0; v < 4; ++v) tot[i][v] += t[v];
+                                for (int part = 0; part < 2; ++part) {
+                                    float t[4];
+                                    mul_f16_16816(t, c0, c1, c2, c3, bf[part][0], bf[part][1]);
+#pragma unroll
+                                    for (int v = 0; v < 4; ++v) tot[i][v] += t[v];
+                                }
                             } else {
                                 mma_f16_16816(acc[i], c0, c1, c2, c3, bf[0][0], bf[0][1]);
                             }
